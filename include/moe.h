@@ -451,6 +451,144 @@ moe_status_t moe_backward(const moe_config_t* cfg, const void* x, const void* dy
                           float* d_ws_gate, float* d_ws_up, float* d_ws_down, void* ws, size_t ws_bytes,
                           moe_stream_t stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * The operators around the routed layer: the norm in front of an FFN
+ * (moe_norm_*), the gate/up projections of a dense FFN block
+ * (moe_gated_*) and the linear layer that closes it, with the residual add
+ * in its epilogue (moe_linear_*).  A dense pre-norm FFN block is
+ *   n = norm(x);  h = act(n Wg^T) * (n Wu^T);  y = h Wd^T + x.
+ * The conventions at the top of this file hold (contiguous, 16-byte aligned
+ * device tensors; stream order; no allocation or synchronisation; errors
+ * returned before anything is enqueued), and besides:
+ *   - biases, norm weights and their gradients are float32, as router_b is;
+ *   - T = 0 is a valid call: outputs of T rows are empty, weight and bias
+ *     gradients are written as zeros;
+ *   - every output is written, none accumulated into, and is a fixed
+ *     function of the inputs, bit for bit (no atomics);
+ *   - a tensor the call writes must not overlap another one of the call,
+ *     except where stated;
+ *   - NaN and infinity propagate as the formulas have them.
+ */
+typedef enum {
+    MOE_ACT_NONE = 0,      /* z                                                   */
+    MOE_ACT_SILU = 1,      /* z / (1 + e^-z)                                      */
+    MOE_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2                         */
+    MOE_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2     */
+    MOE_ACT_RELU = 4       /* max(z, 0); slope 0 at 0                             */
+} moe_act_t;
+
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind_t;
+
+typedef struct {
+    int32_t T;        /* rows, >= 0                                              */
+    int32_t H;        /* elements per row, multiple of 8, at most 16384           */
+    int32_t kind;     /* moe_norm_kind_t                                          */
+    float eps;        /* >= 0, finite                                             */
+    int32_t dtype;    /* moe_dtype_t of x, y, dx and d_residual                   */
+    int32_t dy_dtype; /* moe_dtype_t of dy: dtype, or MOE_F32 (moe_backward's dx) */
+} moe_norm_config_t;
+
+/*
+ * moe_norm_forward -- y = w xh + b, xh = (x - mu) r, over each row of x:
+ * mu the row's mean (0 for MOE_NORM_RMS), r = 1 / sqrt(mean((x - mu)^2) + eps).
+ *   x, y [T, H]; weight [H] or NULL (ones); bias [H] or NULL (zeros);
+ *   mean_out, rstd_out [T] float32 or NULL: mu and r, which moe_norm_backward
+ *   reads (mean_out is not written for MOE_NORM_RMS).  y may be x.
+ * The statistics are float32, from the squared deviations (no difference of
+ * large sums); y is rounded once.  No workspace.
+ */
+moe_status_t moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const float* weight, const float* bias,
+                              void* y, float* mean_out, float* rstd_out, moe_stream_t stream);
+
+/*
+ * moe_norm_backward -- with a = w dy:
+ *   dx = r (a - mean(a) - xh mean(a xh)) + d_residual   (RMS: no mean(a)),
+ *   d_weight = sum over rows of dy xh,  d_bias = sum over rows of dy.
+ *   dy [T, H] in dy_dtype; x, weight as in the forward; mean (NULL for
+ *   MOE_NORM_RMS), rstd [T] as the forward wrote them; d_residual [T, H] or
+ *   NULL: the gradient that reaches x past the norm; d_weight, d_bias [H]
+ *   float32 or NULL to skip.  dx may be d_residual, or dy when both have the
+ *   same type.  ws: moe_norm_workspace_size(cfg) bytes (partial sums).
+ */
+size_t moe_norm_workspace_size(const moe_norm_config_t* cfg);
+moe_status_t moe_norm_backward(const moe_norm_config_t* cfg, const void* dy, const void* x, const float* weight,
+                               const float* mean, const float* rstd, const void* d_residual, void* dx,
+                               float* d_weight, float* d_bias, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+typedef struct {
+    int32_t T;          /* rows (tokens), >= 0                               */
+    int32_t K;          /* input features, multiple of 8                      */
+    int32_t N;          /* output features, multiple of 8                     */
+    int32_t act;        /* moe_act_t                                          */
+    int32_t dtype;      /* MOE_BF16 (MOE_F32: MOE_ERR_UNSUPPORTED)            */
+    int32_t grad_dtype; /* moe_dtype_t of the weight gradients                */
+} moe_dense_config_t;
+
+/* Workspaces of the four calls below: 256-byte aligned, starting with the
+ * device check flags (zeroed before first use, read by
+ * moe_dense_get_device_status); 0 for an invalid cfg (moe_last_error). */
+size_t moe_linear_workspace_size(const moe_dense_config_t* cfg);
+size_t moe_linear_backward_workspace_size(const moe_dense_config_t* cfg);
+size_t moe_gated_workspace_size(const moe_dense_config_t* cfg);
+size_t moe_gated_backward_workspace_size(const moe_dense_config_t* cfg);
+
+/*
+ * moe_linear_forward -- y = act(z) + residual, z = x W^T + bias, in one kernel.
+ *   x [T, K], w [N, K], y [T, N] bf16; bias [N] float32 or NULL; residual
+ *   [T, N] bf16 or NULL; z_out [T, N] bf16 or NULL: z, which
+ *   moe_linear_backward reads when act is not MOE_ACT_NONE.  y may be
+ *   residual.  float32 accumulation; bias, activation and residual are
+ *   applied to the float32 sums and y (and z_out) rounded once.
+ */
+moe_status_t moe_linear_forward(const moe_dense_config_t* cfg, const void* x, const void* w, const float* bias,
+                                const void* residual, void* y, void* z_out, void* ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/*
+ * moe_linear_backward -- with dz = dy act'(z):
+ *   dx = dz W,  d_w = dz^T x,  d_bias = sum over rows of dz
+ * (the residual's gradient is dy itself).
+ *   dy [T, N] bf16; x, w as in the forward; z [T, N] bf16, the forward's
+ *   z_out (NULL when act is MOE_ACT_NONE); dx [T, K] bf16, d_w [N, K] in
+ *   grad_dtype, d_bias [N] float32, each NULL to skip.  dz is rounded to bf16
+ *   where it is an operand of the two products (with MOE_ACT_NONE it is dy,
+ *   unrounded); d_bias is summed from the unrounded values.
+ */
+moe_status_t moe_linear_backward(const moe_dense_config_t* cfg, const void* dy, const void* x, const void* w,
+                                 const void* z, void* dx, void* d_w, float* d_bias, void* ws, size_t ws_bytes,
+                                 moe_stream_t stream);
+
+/*
+ * moe_gated_forward -- h = act(g) * u, g = x W_gate^T + b_gate, u = x W_up^T +
+ * b_up: both projections, the activation and the product in one kernel.
+ *   x [T, K], w_gate, w_up [N, K], h [T, N] bf16; b_gate, b_up [N] float32 or
+ *   NULL; g_out, u_out [T, N] bf16 or NULL: g and u, which
+ *   moe_gated_backward reads.  float32 accumulation; h is formed from the
+ *   float32 sums and each output rounded once.
+ */
+moe_status_t moe_gated_forward(const moe_dense_config_t* cfg, const void* x, const void* w_gate, const void* w_up,
+                               const float* b_gate, const float* b_up, void* h, void* g_out, void* u_out, void* ws,
+                               size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_gated_backward -- with dg = dh u act'(g) and du = dh act(g):
+ *   dx = dg W_gate + du W_up,  d_w_gate = dg^T x,  d_w_up = du^T x,
+ *   d_b_gate, d_b_up = the sums of dg, du over the rows.
+ *   dh, g, u [T, N] bf16 (g, u as the forward wrote them); dx [T, K] bf16,
+ *   d_w_gate and d_w_up [N, K] in grad_dtype (both or neither), d_b_gate, d_b_up [N]
+ *   float32, each NULL to skip.  dg and du are rounded to bf16 as operands of
+ *   the products; the bias gradients are summed from the unrounded values.
+ */
+moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, const void* x, const void* w_gate,
+                                const void* w_up, const void* g, const void* u, void* dx, void* d_w_gate,
+                                void* d_w_up, float* d_b_gate, float* d_b_up, void* ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/* moe_get_device_status for a workspace of the moe_linear_* and moe_gated_*
+ * calls: waits for `stream`, returns and clears its device check flags. */
+moe_status_t moe_dense_get_device_status(void* ws, size_t ws_bytes, moe_stream_t stream, int32_t* flags_out);
+
 /* Waits for `stream`, then returns the device check flags (MOE_DEVFLAG_*)
  * accumulated in `ws` since the last call and clears them.  Returns
  * MOE_ERR_DEVICE_CHECK if any flag was set, MOE_OK otherwise. */

@@ -7,7 +7,9 @@ the library's CUDA kernels.  There is no CPU fallback: if the library is
 missing or cannot load, calls raise ``MoeError``.
 
 ``forward(...)`` is the convenience form of ``moe_forward`` that allocates
-the output and the workspace with torch.
+the output and the workspace with torch; ``norm``, ``linear`` and ``gated``
+are those of the operators around the layer, and ``ffn_block`` /
+``ffn_block_backward`` run them together as a dense pre-norm FFN block.
 """
 from __future__ import annotations
 
@@ -22,6 +24,8 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "M
           4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE_CHECK"}
 DEVFLAG_BAD_EXPERT_INDEX = 0x1
 DEVFLAG_WAIT_TIMEOUT = 0x2
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
+NORMS = {"layer": 0, "rms": 1}
 
 
 class MoeError(RuntimeError):
@@ -34,6 +38,16 @@ class moe_config_t(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("top_k", ctypes.c_int32), ("I_shared", ctypes.c_int32),
                 ("capacity_factor", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class moe_norm_config_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("kind", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("dy_dtype", ctypes.c_int32)]
+
+
+class moe_dense_config_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
 
 
 class moe_trace_record_t(ctypes.Structure):
@@ -67,6 +81,18 @@ _SIGS = {
     "moe_backward_workspace_size": ([ctypes.POINTER(moe_config_t)], ctypes.c_size_t),
     "moe_backward": ([ctypes.POINTER(moe_config_t)] + [_P] * 21 + [ctypes.c_size_t, _P], ctypes.c_int),
     "moe_reduce_partials": ([ctypes.POINTER(moe_config_t), _P, ctypes.c_int32, _P, _P], ctypes.c_int),
+    "moe_norm_forward": ([ctypes.POINTER(moe_norm_config_t)] + [_P] * 7, ctypes.c_int),
+    "moe_norm_workspace_size": ([ctypes.POINTER(moe_norm_config_t)], ctypes.c_size_t),
+    "moe_norm_backward": ([ctypes.POINTER(moe_norm_config_t)] + [_P] * 10 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_linear_workspace_size": ([ctypes.POINTER(moe_dense_config_t)], ctypes.c_size_t),
+    "moe_linear_backward_workspace_size": ([ctypes.POINTER(moe_dense_config_t)], ctypes.c_size_t),
+    "moe_gated_workspace_size": ([ctypes.POINTER(moe_dense_config_t)], ctypes.c_size_t),
+    "moe_gated_backward_workspace_size": ([ctypes.POINTER(moe_dense_config_t)], ctypes.c_size_t),
+    "moe_linear_forward": ([ctypes.POINTER(moe_dense_config_t)] + [_P] * 7 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_linear_backward": ([ctypes.POINTER(moe_dense_config_t)] + [_P] * 8 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_gated_forward": ([ctypes.POINTER(moe_dense_config_t)] + [_P] * 9 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_gated_backward": ([ctypes.POINTER(moe_dense_config_t)] + [_P] * 12 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_dense_get_device_status": ([_P, ctypes.c_size_t, _P, ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
     "moe_get_device_status": ([ctypes.POINTER(moe_config_t), _P, ctypes.c_size_t, _P,
                                ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
     "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -152,6 +178,18 @@ def _stream(stream):
 
         return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _on(stream):
+    """Makes `stream` current for a convenience form's own allocations and
+    fills, so that they are ordered with the kernels it enqueues."""
+    import contextlib
+
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def workspace(cfg: moe_config_t, device="cuda"):
@@ -378,20 +416,308 @@ def moe_trace_end(max_records: int = 4096) -> list[tuple[str, float]]:
     return [(recs[i].name.decode(), recs[i].ms) for i in range(n.value)]
 
 
+# ------------------------------------------------ the operators around the layer
+def _code(table: dict, name: str, what: str) -> int:
+    if name not in table:
+        raise MoeError(1, f"{what} {name!r} unknown: one of {', '.join(table)}")
+    return table[name]
+
+
+_DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16}
+
+
+def norm_config(T: int, H: int, kind: str = "layer", eps: float = 1e-5, dtype: str = "bf16",
+                dy_dtype: str | None = None) -> moe_norm_config_t:
+    """kind "layer" or "rms"; dtype of the rows; dy_dtype (default: dtype) of
+    the backward's upstream gradient."""
+    d = _code(_DTYPES, dtype, "dtype")
+    return moe_norm_config_t(T, H, _code(NORMS, kind, "norm kind"), eps, d,
+                             d if dy_dtype is None else _code(_DTYPES, dy_dtype, "dy_dtype"))
+
+
+def dense_config(T: int, K: int, N: int, act: str = "none", dtype: str = "bf16",
+                 grad_dtype: str = "f32") -> moe_dense_config_t:
+    """T rows of K inputs to N outputs; act one of ACTS; grad_dtype of the
+    weight gradients."""
+    return moe_dense_config_t(T, K, N, _code(ACTS, act, "act"), _code(_DTYPES, dtype, "dtype"),
+                              _code(_DTYPES, grad_dtype, "grad_dtype"))
+
+
+def _arg(t, name: str, shape: tuple, dtype: int, optional: bool = False):
+    """Device pointer of a contiguous tensor of this shape and MOE_* dtype on
+    the current device (ints pass through as raw pointers)."""
+    import torch
+
+    if t is None:
+        if optional:
+            return None
+        raise MoeError(1, f"{name} is None")
+    if isinstance(t, int):
+        return t
+    want = torch.bfloat16 if dtype == MOE_BF16 else torch.float32
+    if t.dtype != want:
+        raise MoeError(1, f"{name} is {t.dtype}, not {want}")
+    if tuple(t.shape) != tuple(shape):
+        raise MoeError(1, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    p = _ptr(t)
+    if t.device.index != torch.cuda.current_device():
+        raise MoeError(1, f"{name} is on {t.device}, not on the current device")
+    return p
+
+
+def _sized(size_fn, cfg) -> int:
+    n = size_fn(ctypes.byref(cfg))
+    if n == 0:
+        raise MoeError(1, load().moe_last_error().decode())
+    return n
+
+
+def _new_ws(nbytes: int, device):
+    """A workspace whose device check flags (its first bytes) are clear."""
+    import torch
+
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def moe_norm_workspace_size(cfg) -> int:
+    return _sized(load().moe_norm_workspace_size, cfg)
+
+
+def moe_linear_workspace_size(cfg) -> int:
+    return _sized(load().moe_linear_workspace_size, cfg)
+
+
+def moe_linear_backward_workspace_size(cfg) -> int:
+    return _sized(load().moe_linear_backward_workspace_size, cfg)
+
+
+def moe_gated_workspace_size(cfg) -> int:
+    return _sized(load().moe_gated_workspace_size, cfg)
+
+
+def moe_gated_backward_workspace_size(cfg) -> int:
+    return _sized(load().moe_gated_backward_workspace_size, cfg)
+
+
+def norm_workspace(cfg, device="cuda"):
+    return _new_ws(moe_norm_workspace_size(cfg), device)
+
+
+def linear_workspace(cfg, device="cuda"):
+    return _new_ws(moe_linear_workspace_size(cfg), device)
+
+
+def linear_backward_workspace(cfg, device="cuda"):
+    return _new_ws(moe_linear_backward_workspace_size(cfg), device)
+
+
+def gated_workspace(cfg, device="cuda"):
+    return _new_ws(moe_gated_workspace_size(cfg), device)
+
+
+def gated_backward_workspace(cfg, device="cuda"):
+    return _new_ws(moe_gated_backward_workspace_size(cfg), device)
+
+
+def moe_norm_forward(cfg, x, weight, bias, y, mean_out=None, rstd_out=None, stream=None):
+    """y = norm(x); mean_out, rstd_out [T] float32 keep the statistics."""
+    T, H, d = cfg.T, cfg.H, cfg.dtype
+    _check(load().moe_norm_forward(ctypes.byref(cfg), _arg(x, "x", (T, H), d),
+                                   _arg(weight, "weight", (H,), MOE_F32, True),
+                                   _arg(bias, "bias", (H,), MOE_F32, True), _arg(y, "y", (T, H), d),
+                                   _arg(mean_out, "mean_out", (T,), MOE_F32, True),
+                                   _arg(rstd_out, "rstd_out", (T,), MOE_F32, True), _stream(stream)))
+
+
+def moe_norm_backward(cfg, dy, x, weight, mean, rstd, d_residual, dx, d_weight, d_bias, ws, stream=None):
+    """dx (+ d_residual), d_weight and d_bias (each may be None) of the norm."""
+    T, H, d = cfg.T, cfg.H, cfg.dtype
+    p, n = _ws(ws)
+    _check(load().moe_norm_backward(ctypes.byref(cfg), _arg(dy, "dy", (T, H), cfg.dy_dtype),
+                                    _arg(x, "x", (T, H), d), _arg(weight, "weight", (H,), MOE_F32, True),
+                                    _arg(mean, "mean", (T,), MOE_F32, True), _arg(rstd, "rstd", (T,), MOE_F32),
+                                    _arg(d_residual, "d_residual", (T, H), d, True), _arg(dx, "dx", (T, H), d),
+                                    _arg(d_weight, "d_weight", (H,), MOE_F32, True),
+                                    _arg(d_bias, "d_bias", (H,), MOE_F32, True), p, n, _stream(stream)))
+
+
+def moe_linear_forward(cfg, x, w, bias, residual, y, z_out=None, ws=None, stream=None):
+    """y = act(x w^T + bias) + residual; z_out keeps the pre-activations."""
+    T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
+    _check(load().moe_linear_forward(ctypes.byref(cfg), _arg(x, "x", (T, K), d), _arg(w, "w", (N, K), d),
+                                     _arg(bias, "bias", (N,), MOE_F32, True),
+                                     _arg(residual, "residual", (T, N), d, True), _arg(y, "y", (T, N), d),
+                                     _arg(z_out, "z_out", (T, N), d, True), *_ws(ws), _stream(stream)))
+
+
+def moe_linear_backward(cfg, dy, x, w, z, dx, d_w, d_bias, ws=None, stream=None):
+    """dx, d_w, d_bias (each may be None) of the linear layer."""
+    T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
+    _check(load().moe_linear_backward(ctypes.byref(cfg), _arg(dy, "dy", (T, N), d),
+                                      _arg(x, "x", (T, K), d, d_w is None), _arg(w, "w", (N, K), d, dx is None),
+                                      _arg(z, "z", (T, N), d, True), _arg(dx, "dx", (T, K), d, True),
+                                      _arg(d_w, "d_w", (N, K), cfg.grad_dtype, True),
+                                      _arg(d_bias, "d_bias", (N,), MOE_F32, True), *_ws(ws), _stream(stream)))
+
+
+def moe_gated_forward(cfg, x, w_gate, w_up, b_gate, b_up, h, g_out=None, u_out=None, ws=None, stream=None):
+    """h = act(x w_gate^T + b_gate) * (x w_up^T + b_up); g_out, u_out keep the
+    two projections."""
+    T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
+    _check(load().moe_gated_forward(ctypes.byref(cfg), _arg(x, "x", (T, K), d), _arg(w_gate, "w_gate", (N, K), d),
+                                    _arg(w_up, "w_up", (N, K), d), _arg(b_gate, "b_gate", (N,), MOE_F32, True),
+                                    _arg(b_up, "b_up", (N,), MOE_F32, True), _arg(h, "h", (T, N), d),
+                                    _arg(g_out, "g_out", (T, N), d, True), _arg(u_out, "u_out", (T, N), d, True),
+                                    *_ws(ws), _stream(stream)))
+
+
+def moe_gated_backward(cfg, dh, x, w_gate, w_up, g, u, dx, d_w_gate, d_w_up, d_b_gate=None, d_b_up=None, ws=None,
+                       stream=None):
+    """dx, the two weight gradients and the two bias gradients (each may be
+    None) of the gate/up projections."""
+    T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
+    no_dw = d_w_gate is None and d_w_up is None
+    _check(load().moe_gated_backward(
+        ctypes.byref(cfg), _arg(dh, "dh", (T, N), d), _arg(x, "x", (T, K), d, no_dw),
+        _arg(w_gate, "w_gate", (N, K), d, dx is None), _arg(w_up, "w_up", (N, K), d, dx is None),
+        _arg(g, "g", (T, N), d), _arg(u, "u", (T, N), d), _arg(dx, "dx", (T, K), d, True),
+        _arg(d_w_gate, "d_w_gate", (N, K), cfg.grad_dtype, True), _arg(d_w_up, "d_w_up", (N, K), cfg.grad_dtype, True),
+        _arg(d_b_gate, "d_b_gate", (N,), MOE_F32, True), _arg(d_b_up, "d_b_up", (N,), MOE_F32, True), *_ws(ws),
+        _stream(stream)))
+
+
+def moe_dense_get_device_status(ws, stream=None) -> int:
+    """moe_get_device_status for a workspace of the linear and gated calls."""
+    flags = ctypes.c_int32(0)
+    st = load().moe_dense_get_device_status(*_ws(ws), _stream(stream), ctypes.byref(flags))
+    if st not in (0, 5):
+        _check(st)
+    return flags.value
+
+
+def _dtype_name(t) -> str:
+    import torch
+
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise MoeError(1, f"{t.dtype} tensors are not supported")
+    return "bf16" if t.dtype == torch.bfloat16 else "f32"
+
+
+def norm(x, weight=None, bias=None, eps: float = 1e-5, kind: str = "layer", mean_out=None, rstd_out=None,
+         stream=None):
+    """moe_norm_forward into a new tensor."""
+    import torch
+
+    T, H = x.shape
+    with _on(stream):
+        y = torch.empty_like(x)
+        moe_norm_forward(norm_config(T, H, kind, eps, _dtype_name(x)), x, weight, bias, y, mean_out, rstd_out)
+    return y
+
+
+def linear(x, w, bias=None, residual=None, act: str = "none", z_out=None, ws=None, stream=None):
+    """moe_linear_forward into a new tensor."""
+    import torch
+
+    cfg = dense_config(x.shape[0], x.shape[1], w.shape[0], act, _dtype_name(x))
+    with _on(stream):
+        ws = linear_workspace(cfg, x.device) if ws is None else ws
+        y = torch.empty((cfg.T, cfg.N), dtype=x.dtype, device=x.device)
+        moe_linear_forward(cfg, x, w, bias, residual, y, z_out, ws)
+    return y
+
+
+def gated(x, w_gate, w_up, b_gate=None, b_up=None, act: str = "silu", g_out=None, u_out=None, ws=None, stream=None):
+    """moe_gated_forward into a new tensor."""
+    import torch
+
+    cfg = dense_config(x.shape[0], x.shape[1], w_gate.shape[0], act, _dtype_name(x))
+    with _on(stream):
+        ws = gated_workspace(cfg, x.device) if ws is None else ws
+        h = torch.empty((cfg.T, cfg.N), dtype=x.dtype, device=x.device)
+        moe_gated_forward(cfg, x, w_gate, w_up, b_gate, b_up, h, g_out, u_out, ws)
+    return h
+
+
+def ffn_block(x, norm_w, w_gate, w_up, w_down, norm_b=None, kind: str = "rms", eps: float = 1e-5, act: str = "silu",
+              keep: bool = False, stream=None):
+    """A dense pre-norm FFN block, y = x + (act(n w_gate^T) * (n w_up^T)) w_down^T
+    with n = norm(x): the dense layers between routed ones.  x [T, H] bf16,
+    w_gate, w_up [I, H], w_down [H, I], norm_w, norm_b [H] float32 or None.
+    keep: returns (y, kept), kept being what ffn_block_backward reads."""
+    import torch
+
+    T, H = x.shape
+    I = w_gate.shape[0]
+    dev = x.device
+    mean = rstd = g = u = None
+    with _on(stream):
+        if keep:
+            mean, rstd = torch.empty((2, (T + 3) // 4 * 4), dtype=torch.float32, device=dev)[:, :T].unbind()
+            g, u = (torch.empty((T, I), dtype=x.dtype, device=dev) for _ in range(2))
+        n = norm(x, norm_w, norm_b, eps, kind, mean, rstd)
+        h = gated(n, w_gate, w_up, act=act, g_out=g, u_out=u)
+        y = linear(h, w_down, residual=x)
+    if not keep:
+        return y
+    return y, dict(x=x, n=n, g=g, u=u, h=h, mean=mean, rstd=rstd, norm_w=norm_w, has_norm_b=norm_b is not None,
+                   w_gate=w_gate, w_up=w_up, w_down=w_down, kind=kind, eps=eps, act=act)
+
+
+def ffn_block_backward(dy, kept, grad_dtype: str = "f32", stream=None) -> dict:
+    """Every gradient of ffn_block for the upstream gradient dy [T, H] bf16:
+    dx, d_norm_w, d_norm_b (None without the bias), d_w_gate, d_w_up, d_w_down
+    (in grad_dtype)."""
+    import torch
+
+    k = kept
+    x, h, n = k["x"], k["h"], k["n"]
+    (T, H), I, dev = x.shape, h.shape[1], x.device
+    gt = torch.float32 if grad_dtype == "f32" else torch.bfloat16
+    with _on(stream):
+        dh, dn, dx = torch.empty_like(h), torch.empty_like(n), torch.empty_like(x)
+        out = dict(dx=dx, d_norm_w=None, d_norm_b=None, d_w_gate=torch.empty((I, H), dtype=gt, device=dev),
+                   d_w_up=torch.empty((I, H), dtype=gt, device=dev), d_w_down=torch.empty((H, I), dtype=gt, device=dev))
+        for name, has in (("d_norm_w", k["norm_w"] is not None), ("d_norm_b", k["has_norm_b"])):
+            if has:
+                out[name] = torch.empty(H, dtype=torch.float32, device=dev)
+        cfg = dense_config(T, I, H, "none", "bf16", grad_dtype)
+        moe_linear_backward(cfg, dy, h, k["w_down"], None, dh, out["d_w_down"], None,
+                            linear_backward_workspace(cfg, dev))
+        cfg = dense_config(T, H, I, k["act"], "bf16", grad_dtype)
+        moe_gated_backward(cfg, dh, n, k["w_gate"], k["w_up"], k["g"], k["u"], dn, out["d_w_gate"], out["d_w_up"],
+                           ws=gated_backward_workspace(cfg, dev))
+        cfg = norm_config(T, H, k["kind"], k["eps"], "bf16")
+        moe_norm_backward(cfg, dn, x, k["norm_w"], k["mean"] if k["kind"] == "layer" else None, k["rstd"], dy, dx,
+                          out["d_norm_w"], out["d_norm_b"], norm_workspace(cfg, dev))
+    return out
+
+
 def forward(x, router_w, w_gate, w_up, w_down, top_k: int, router_b=None, ws_gate=None, ws_up=None,
             ws_down=None, capacity_factor: float = 0.0, ws=None, topk_idx_out=None, counts_out=None,
-            dropped_out=None, stream=None):
-    """y = MoE(x): the pages' moe_forward(x, experts, router, top_k) on the GPU."""
+            dropped_out=None, stream=None, norm_w=None, norm_b=None, norm_kind: str | None = None,
+            norm_eps: float = 1e-5):
+    """y = MoE(x): the pages' moe_forward(x, experts, router, top_k) on the GPU.
+    norm_kind "layer" or "rms": y = MoE(norm(x)), the layer behind its
+    pre-norm (moe_norm_forward with norm_w, norm_b, norm_eps)."""
     import torch
+
+    if norm_kind is None and (norm_w is not None or norm_b is not None):
+        raise MoeError(1, "norm_w and norm_b need norm_kind")
 
     T, H = x.shape
     E, I, _ = w_gate.shape
     Is = 0 if ws_gate is None else ws_gate.shape[0]
     dtype = "bf16" if x.dtype == torch.bfloat16 else "f32"
     cfg = config(T, H, I, E, top_k, Is, capacity_factor, dtype)
-    if ws is None:
-        ws = workspace(cfg, x.device)
-    y = torch.empty_like(x)
-    moe_forward(cfg, x, router_w, router_b, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, y,
-                topk_idx_out, counts_out, dropped_out, ws, stream)
+    with _on(stream):
+        if norm_kind is not None:
+            x = norm(x, norm_w, norm_b, norm_eps, norm_kind)
+        if ws is None:
+            ws = workspace(cfg, x.device)
+        y = torch.empty_like(x)
+        moe_forward(cfg, x, router_w, router_b, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, y,
+                    topk_idx_out, counts_out, dropped_out, ws)
     return y

@@ -1,0 +1,68 @@
+// Activations of the gate/up projections and the linear layer, float32.
+#pragma once
+
+#include <type_traits>
+
+#include "common.cuh"
+
+namespace moe {
+
+// p(z) = 1 / (1 + e^-z) through the fast exponential: an infinite e^-z gives 0.
+__device__ __forceinline__ float sigmoid_f32(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+// sqrt(2 / pi) (z + 0.044715 z^3), doubled: tanh-form GELU is z sigmoid(this).
+__device__ __forceinline__ float gelu_tanh_arg(float z) {
+    return 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
+}
+
+// act(z).  __fdividef(1, y) is 0 for y above 2^126, where the sigmoid is below
+// every float32 normal anyway.  ReLU keeps a NaN.
+template <int kAct>
+__device__ __forceinline__ float act_value(float z) {
+    if (kAct == MOE_ACT_SILU) return z * sigmoid_f32(z);
+    if (kAct == MOE_ACT_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    if (kAct == MOE_ACT_GELU_TANH) return z * sigmoid_f32(gelu_tanh_arg(z));
+    if (kAct == MOE_ACT_RELU) return z < 0.f ? 0.f : z;
+    return z;
+}
+
+// act(z) and act'(z).  The slope of the tanh form is p + z p (1 - p) q' with q'
+// quadratic in z: beyond |z| = 30, where p (1 - p) is 0, z is clamped so that
+// no 0 * inf arises.
+template <int kAct>
+__device__ __forceinline__ void act_slope(float z, float& a, float& d) {
+    if (kAct == MOE_ACT_SILU) {
+        const float p = sigmoid_f32(z);
+        a = z * p;
+        d = p * fmaf(z, 1.f - p, 1.f);
+    } else if (kAct == MOE_ACT_GELU) {
+        const float c = 0.5f * erfcf(-0.70710678118654752f * z);
+        a = z * c;
+        d = fmaf(z, 0.3989422804014327f * __expf(-0.5f * z * z), c);
+    } else if (kAct == MOE_ACT_GELU_TANH) {
+        const float p = sigmoid_f32(gelu_tanh_arg(z));
+        const float c = fminf(fmaxf(z, -30.f), 30.f);
+        a = z * p;
+        d = fmaf(c * p * (1.f - p), 1.5957691216057308f * fmaf(0.134145f * c, c, 1.f), p);
+    } else if (kAct == MOE_ACT_RELU) {
+        a = z < 0.f ? 0.f : z;
+        d = z > 0.f ? 1.f : 0.f;
+    } else {
+        a = z;
+        d = 1.f;
+    }
+}
+
+// f(std::integral_constant<int, act>) for a run-time activation (a uniform branch).
+template <typename F>
+__host__ __device__ __forceinline__ void by_act(int act, F f) {
+    switch (act) {
+        case MOE_ACT_SILU: f(std::integral_constant<int, MOE_ACT_SILU>()); break;
+        case MOE_ACT_GELU: f(std::integral_constant<int, MOE_ACT_GELU>()); break;
+        case MOE_ACT_GELU_TANH: f(std::integral_constant<int, MOE_ACT_GELU_TANH>()); break;
+        case MOE_ACT_RELU: f(std::integral_constant<int, MOE_ACT_RELU>()); break;
+        default: f(std::integral_constant<int, MOE_ACT_NONE>()); break;
+    }
+}
+
+}  // namespace moe

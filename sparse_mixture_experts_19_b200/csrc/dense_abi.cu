@@ -1,0 +1,350 @@
+// C ABI of the operators around the routed layer (norm, linear, gated):
+// argument checks, workspace carving and launch sequencing.  Like moe_abi.cu:
+// nothing here allocates device memory or synchronises, except
+// moe_dense_get_device_status (documented to wait).
+#include <math.h>
+
+#include "abi_util.cuh"
+#include "dense.cuh"
+
+namespace moe {
+namespace {
+
+moe_status_t check_norm(const moe_norm_config_t* c) {
+    if (!c) return fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
+    if (c->T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", c->T);
+    if (c->H < 8 || c->H % 8) return fail(MOE_ERR_INVALID_ARG, "H = %d must be a positive multiple of 8", c->H);
+    if (c->kind != MOE_NORM_LAYER && c->kind != MOE_NORM_RMS)
+        return fail(MOE_ERR_INVALID_ARG, "kind = %d unknown", c->kind);
+    if (!isfinite(c->eps) || c->eps < 0.f) return fail(MOE_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "dtype = %d unknown", c->dtype);
+    if (c->dy_dtype != MOE_F32 && c->dy_dtype != MOE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "dy_dtype = %d unknown", c->dy_dtype);
+    if (c->dtype == MOE_F32 && c->dy_dtype != MOE_F32)
+        return fail(MOE_ERR_UNSUPPORTED, "float32 rows take a float32 dy");
+    if (c->H > kMaxNormWidth) return fail(MOE_ERR_UNSUPPORTED, "H = %d above %d", c->H, kMaxNormWidth);
+    return MOE_OK;
+}
+
+size_t norm_ws_bytes(const moe_norm_config_t* c) {
+    return align_up(sizeof(float) * 2 * c->H * (c->T > 0 ? norm_bwd_blocks(c->T, c->H) : 1));
+}
+
+moe_status_t check_dense(const moe_dense_config_t* c) {
+    if (!c) return fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
+    if (c->T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", c->T);
+    if (c->K < 8 || c->K % 8) return fail(MOE_ERR_INVALID_ARG, "K = %d must be a positive multiple of 8", c->K);
+    if (c->N < 8 || c->N % 8) return fail(MOE_ERR_INVALID_ARG, "N = %d must be a positive multiple of 8", c->N);
+    if (c->act < MOE_ACT_NONE || c->act > MOE_ACT_RELU) return fail(MOE_ERR_INVALID_ARG, "act = %d unknown", c->act);
+    if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "dtype = %d unknown", c->dtype);
+    if (c->grad_dtype != MOE_F32 && c->grad_dtype != MOE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "grad_dtype = %d unknown", c->grad_dtype);
+    if (c->dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "the dense products take bf16 tensors");
+    return MOE_OK;
+}
+
+// Pieces of a dense workspace.
+struct DensePlan {
+    int32_t* flags;
+    bf16* dz0;   // [T, N], unless the linear layer has no activation
+    bf16* dz1;   // gated
+    float* sums; // partial bias gradients
+    float* part; // partial weight gradients
+    size_t bytes;
+};
+
+void make_dense_plan(const moe_dense_config_t* c, bool gated, bool backward, void* ws, DensePlan* p) {
+    size_t off = 0;
+    char* base = (char*)ws;
+    auto take = [&](size_t bytes) -> void* {
+        void* r = base ? base + off : nullptr;
+        off += align_up(bytes);
+        return r;
+    };
+    *p = DensePlan{};
+    p->flags = (int32_t*)take(64);
+    if (backward && c->T > 0) {
+        const size_t tn = (size_t)c->T * c->N;
+        const int problems = gated ? 2 : 1;
+        if (gated || c->act != MOE_ACT_NONE) p->dz0 = (bf16*)take(tn * 2);
+        if (gated) p->dz1 = (bf16*)take(tn * 2);
+        p->sums = (float*)take(sizeof(float) * problems * c->N * dense_dz_row_blocks(c->T, c->N));
+        p->part = (float*)take(sizeof(float) * dense_wgrad_part_floats(c->T, c->K, c->N, problems));
+    }
+    p->bytes = off;
+}
+
+moe_status_t dense_plan_for(const moe_dense_config_t* c, bool gated, bool backward, void* ws, size_t ws_bytes,
+                            DensePlan* p) {
+    moe_status_t s = check_dense(c);
+    if (s != MOE_OK) return s;
+    make_dense_plan(c, gated, backward, nullptr, p);
+    if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)ws % kWsAlign) return fail(MOE_ERR_WORKSPACE, "workspace not %d-byte aligned", kWsAlign);
+    if (ws_bytes < p->bytes)
+        return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, p->bytes);
+    make_dense_plan(c, gated, backward, ws, p);
+    return MOE_OK;
+}
+
+size_t dense_ws_size(const moe_dense_config_t* c, bool gated, bool backward) {
+    if (check_dense(c) != MOE_OK) return 0;
+    DensePlan p;
+    make_dense_plan(c, gated, backward, nullptr, &p);
+    return p.bytes;
+}
+
+size_t grad_bytes(const moe_dense_config_t* c) {
+    return (size_t)c->N * c->K * (c->grad_dtype == MOE_F32 ? 4 : 2);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+#define NOT_SAME(a, b)                                                                          \
+    do {                                                                                        \
+        if ((a) && (const void*)(a) == (const void*)(b))                                        \
+            return fail(MOE_ERR_INVALID_ARG, "%s and %s are the same tensor", #a, #b);          \
+    } while (0)
+
+extern "C" {
+
+size_t moe_norm_workspace_size(const moe_norm_config_t* cfg) {
+    return check_norm(cfg) == MOE_OK ? norm_ws_bytes(cfg) : 0;
+}
+
+moe_status_t moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const float* weight, const float* bias,
+                              void* y, float* mean_out, float* rstd_out, moe_stream_t stream) {
+    moe_status_t s = check_norm(cfg);
+    if (s != MOE_OK) return s;
+    OPTIONAL_PTR(weight);
+    OPTIONAL_PTR(bias);
+    OPTIONAL_PTR(mean_out);
+    OPTIONAL_PTR(rstd_out);
+    if (cfg->T == 0) return MOE_OK;
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(y);
+    NormArgs a{};
+    a.T = cfg->T;
+    a.H = cfg->H;
+    a.layer = cfg->kind == MOE_NORM_LAYER;
+    a.eps = cfg->eps;
+    a.x = x;
+    a.w = weight;
+    a.b = bias;
+    a.y = y;
+    a.mean_out = mean_out;
+    a.rstd_out = rstd_out;
+    CUDA_TRY(launch_norm_fwd(a, cfg->dtype == MOE_F32, (cudaStream_t)stream), "norm_fwd");
+    return MOE_OK;
+}
+
+moe_status_t moe_norm_backward(const moe_norm_config_t* cfg, const void* dy, const void* x, const float* weight,
+                               const float* mean, const float* rstd, const void* d_residual, void* dx,
+                               float* d_weight, float* d_bias, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    moe_status_t s = check_norm(cfg);
+    if (s != MOE_OK) return s;
+    if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)ws % kWsAlign) return fail(MOE_ERR_WORKSPACE, "workspace not %d-byte aligned", kWsAlign);
+    if (ws_bytes < norm_ws_bytes(cfg))
+        return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, norm_ws_bytes(cfg));
+    OPTIONAL_PTR(weight);
+    OPTIONAL_PTR(d_residual);
+    OPTIONAL_PTR(d_weight);
+    OPTIONAL_PTR(d_bias);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (cfg->T == 0) {
+        if (d_weight) CUDA_TRY(cudaMemsetAsync(d_weight, 0, sizeof(float) * cfg->H, st), "memset");
+        if (d_bias) CUDA_TRY(cudaMemsetAsync(d_bias, 0, sizeof(float) * cfg->H, st), "memset");
+        return MOE_OK;
+    }
+    REQUIRE_PTR(dy);
+    REQUIRE_PTR(x);
+    if (cfg->kind == MOE_NORM_LAYER) REQUIRE_PTR(mean);
+    REQUIRE_PTR(rstd);
+    REQUIRE_PTR(dx);
+    if (cfg->dy_dtype != cfg->dtype) NOT_SAME(dx, dy);
+    NormArgs a{};
+    a.T = cfg->T;
+    a.H = cfg->H;
+    a.layer = cfg->kind == MOE_NORM_LAYER;
+    a.x = x;
+    a.w = weight;
+    a.dy = dy;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.d_res = d_residual;
+    a.dx = dx;
+    a.part = d_weight || d_bias ? (float*)ws : nullptr;
+    a.dw_out = d_weight;
+    a.db_out = d_bias;
+    CUDA_TRY(launch_norm_bwd(a, cfg->dtype == MOE_F32, cfg->dy_dtype == MOE_F32, st), "norm_bwd");
+    return MOE_OK;
+}
+
+size_t moe_linear_workspace_size(const moe_dense_config_t* cfg) { return dense_ws_size(cfg, false, false); }
+size_t moe_linear_backward_workspace_size(const moe_dense_config_t* cfg) { return dense_ws_size(cfg, false, true); }
+size_t moe_gated_workspace_size(const moe_dense_config_t* cfg) { return dense_ws_size(cfg, true, false); }
+size_t moe_gated_backward_workspace_size(const moe_dense_config_t* cfg) { return dense_ws_size(cfg, true, true); }
+
+moe_status_t moe_linear_forward(const moe_dense_config_t* cfg, const void* x, const void* w, const float* bias,
+                                const void* residual, void* y, void* z_out, void* ws, size_t ws_bytes,
+                                moe_stream_t stream) {
+    DensePlan p;
+    moe_status_t s = dense_plan_for(cfg, false, false, ws, ws_bytes, &p);
+    if (s != MOE_OK) return s;
+    if (cfg->T == 0) return MOE_OK;
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(w);
+    OPTIONAL_PTR(bias);
+    OPTIONAL_PTR(residual);
+    REQUIRE_PTR(y);
+    OPTIONAL_PTR(z_out);
+    NOT_SAME(y, x);
+    NOT_SAME(z_out, x);
+    NOT_SAME(z_out, y);
+    NOT_SAME(z_out, residual);
+    DenseOut o{};
+    o.act = cfg->act;
+    o.bias0 = bias;
+    o.res = (const bf16*)residual;
+    o.y = (bf16*)y;
+    o.z0 = (bf16*)z_out;
+    CUDA_TRY(launch_dense_fwd(x, w, nullptr, cfg->T, cfg->K, cfg->N, o, p.flags, (cudaStream_t)stream), "linear_fwd");
+    return MOE_OK;
+}
+
+moe_status_t moe_linear_backward(const moe_dense_config_t* cfg, const void* dy, const void* x, const void* w,
+                                 const void* z, void* dx, void* d_w, float* d_bias, void* ws, size_t ws_bytes,
+                                 moe_stream_t stream) {
+    DensePlan p;
+    moe_status_t s = dense_plan_for(cfg, false, true, ws, ws_bytes, &p);
+    if (s != MOE_OK) return s;
+    OPTIONAL_PTR(dx);
+    OPTIONAL_PTR(d_w);
+    OPTIONAL_PTR(d_bias);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (cfg->T == 0) {
+        if (d_w) CUDA_TRY(cudaMemsetAsync(d_w, 0, grad_bytes(cfg), st), "memset");
+        if (d_bias) CUDA_TRY(cudaMemsetAsync(d_bias, 0, sizeof(float) * cfg->N, st), "memset");
+        return MOE_OK;
+    }
+    const bool act = cfg->act != MOE_ACT_NONE;
+    REQUIRE_PTR(dy);
+    if (d_w) REQUIRE_PTR(x);
+    if (dx) REQUIRE_PTR(w);
+    if (act) REQUIRE_PTR(z);
+    NOT_SAME(dx, dy);
+    NOT_SAME(dx, x);
+    const bf16* dz = act ? p.dz0 : (const bf16*)dy;
+    if (d_bias || (act && (dx || d_w))) {
+        DenseDzArgs a{};
+        a.T = cfg->T;
+        a.N = cfg->N;
+        a.dy = (const bf16*)dy;
+        a.z = (const bf16*)z;
+        a.dz = act ? p.dz0 : nullptr;
+        a.part = p.sums;
+        CUDA_TRY(launch_dense_dz(a, false, cfg->act, d_bias, nullptr, st), "linear_dz");
+    }
+    if (dx) CUDA_TRY(launch_dense_dgrad(dz, nullptr, w, nullptr, cfg->T, cfg->K, cfg->N, dx, p.flags, st), "linear_dgrad");
+    if (d_w)
+        CUDA_TRY(launch_dense_wgrad(dz, nullptr, x, cfg->T, cfg->K, cfg->N, d_w, nullptr, cfg->grad_dtype == MOE_F32,
+                                    p.part, p.flags, st),
+                 "linear_wgrad");
+    return MOE_OK;
+}
+
+moe_status_t moe_gated_forward(const moe_dense_config_t* cfg, const void* x, const void* w_gate, const void* w_up,
+                               const float* b_gate, const float* b_up, void* h, void* g_out, void* u_out, void* ws,
+                               size_t ws_bytes, moe_stream_t stream) {
+    DensePlan p;
+    moe_status_t s = dense_plan_for(cfg, true, false, ws, ws_bytes, &p);
+    if (s != MOE_OK) return s;
+    if (cfg->T == 0) return MOE_OK;
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(w_gate);
+    REQUIRE_PTR(w_up);
+    OPTIONAL_PTR(b_gate);
+    OPTIONAL_PTR(b_up);
+    REQUIRE_PTR(h);
+    OPTIONAL_PTR(g_out);
+    OPTIONAL_PTR(u_out);
+    NOT_SAME(h, x);
+    NOT_SAME(g_out, h);
+    NOT_SAME(u_out, h);
+    NOT_SAME(g_out, u_out);
+    NOT_SAME(g_out, x);
+    NOT_SAME(u_out, x);
+    DenseOut o{};
+    o.act = cfg->act;
+    o.bias0 = b_gate;
+    o.bias1 = b_up;
+    o.y = (bf16*)h;
+    o.z0 = (bf16*)g_out;
+    o.z1 = (bf16*)u_out;
+    CUDA_TRY(launch_dense_fwd(x, w_gate, w_up, cfg->T, cfg->K, cfg->N, o, p.flags, (cudaStream_t)stream), "gated_fwd");
+    return MOE_OK;
+}
+
+moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, const void* x, const void* w_gate,
+                                const void* w_up, const void* g, const void* u, void* dx, void* d_w_gate,
+                                void* d_w_up, float* d_b_gate, float* d_b_up, void* ws, size_t ws_bytes,
+                                moe_stream_t stream) {
+    DensePlan p;
+    moe_status_t s = dense_plan_for(cfg, true, true, ws, ws_bytes, &p);
+    if (s != MOE_OK) return s;
+    OPTIONAL_PTR(dx);
+    OPTIONAL_PTR(d_w_gate);
+    OPTIONAL_PTR(d_w_up);
+    OPTIONAL_PTR(d_b_gate);
+    OPTIONAL_PTR(d_b_up);
+    if (!d_w_gate != !d_w_up) return fail(MOE_ERR_INVALID_ARG, "d_w_gate and d_w_up go together");
+    NOT_SAME(d_w_gate, d_w_up);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (cfg->T == 0) {
+        if (d_w_gate) CUDA_TRY(cudaMemsetAsync(d_w_gate, 0, grad_bytes(cfg), st), "memset");
+        if (d_w_up) CUDA_TRY(cudaMemsetAsync(d_w_up, 0, grad_bytes(cfg), st), "memset");
+        if (d_b_gate) CUDA_TRY(cudaMemsetAsync(d_b_gate, 0, sizeof(float) * cfg->N, st), "memset");
+        if (d_b_up) CUDA_TRY(cudaMemsetAsync(d_b_up, 0, sizeof(float) * cfg->N, st), "memset");
+        return MOE_OK;
+    }
+    REQUIRE_PTR(dh);
+    REQUIRE_PTR(g);
+    REQUIRE_PTR(u);
+    if (d_w_gate) REQUIRE_PTR(x);
+    if (dx) {
+        REQUIRE_PTR(w_gate);
+        REQUIRE_PTR(w_up);
+    }
+    NOT_SAME(dx, x);
+    DenseDzArgs a{};
+    a.T = cfg->T;
+    a.N = cfg->N;
+    a.dy = (const bf16*)dh;
+    a.z = (const bf16*)g;
+    a.u = (const bf16*)u;
+    a.dz = p.dz0;
+    a.dz1 = p.dz1;
+    a.part = p.sums;
+    CUDA_TRY(launch_dense_dz(a, true, cfg->act, d_b_gate, d_b_up, st), "gated_dgu");
+    if (dx)
+        CUDA_TRY(launch_dense_dgrad(p.dz0, p.dz1, w_gate, w_up, cfg->T, cfg->K, cfg->N, dx, p.flags, st),
+                 "gated_dgrad");
+    if (d_w_gate)
+        CUDA_TRY(launch_dense_wgrad(p.dz0, p.dz1, x, cfg->T, cfg->K, cfg->N, d_w_gate, d_w_up,
+                                    cfg->grad_dtype == MOE_F32, p.part, p.flags, st),
+                 "gated_wgrad");
+    return MOE_OK;
+}
+
+moe_status_t moe_dense_get_device_status(void* ws, size_t ws_bytes, moe_stream_t stream, int32_t* flags_out) {
+    if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)ws % kWsAlign) return fail(MOE_ERR_WORKSPACE, "workspace not %d-byte aligned", kWsAlign);
+    if (ws_bytes < kWsAlign) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %d", ws_bytes, kWsAlign);
+    return read_device_flags((int32_t*)ws, (cudaStream_t)stream, flags_out);
+}
+
+}  // extern "C"

@@ -1,0 +1,169 @@
+// Elementwise half of the linear and gate/up backward passes (sm_100a): the
+// gradients of the pre-activations and the bias gradients.
+//
+//   linear: dz = dy act'(z);            db = sum over tokens of dz
+//   gated:  dg = dh u act'(g), du = dh act(g);  dbg, dbu their sums
+//
+// Bound by HBM: each input is read once and dz (dg, du) written once, rounded
+// to bf16 because it is an operand of the tensor-core products that follow;
+// the bias gradients are summed from the unrounded float32 values.  A thread
+// owns 8 columns (one 16-byte access per tensor and row) and walks every 8th
+// row of its block's range; the block adds its 8 row lanes in shared memory
+// and writes one partial row, which launch_sum_partials adds in order.
+#include <algorithm>
+
+#include "act.cuh"
+#include "dense.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kCols = 256;  // columns per block: 32 threads x 8
+constexpr int kLanes = 8;   // row lanes per block
+
+__device__ __forceinline__ void unpack8(const uint4& a, float (&v)[8]) {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// kAct: the activation; kGated: dg and du from dh, g, u; kStore: write dz
+// (false: column sums of dy alone, kAct none).
+template <int kAct, bool kGated, bool kStore>
+__global__ void __launch_bounds__(32 * kLanes) dense_dz_kernel(const DenseDzArgs a) {
+    __shared__ float red[kLanes][kCols + 4];
+    const int c = blockIdx.x * kCols + threadIdx.x * 8;
+    const int64_t r0 = (int64_t)blockIdx.y * a.rows_per_block;
+    const int64_t r1 = min(r0 + a.rows_per_block, (int64_t)a.T);
+    float s0[8] = {}, s1[8] = {};
+    if (c < a.N) {
+        for (int64_t r = r0 + threadIdx.y; r < r1; r += kLanes) {
+            const int64_t o = r * a.N + c;
+            float d[8], z[8], u[8];
+            unpack8(*reinterpret_cast<const uint4*>(a.dy + o), d);
+            if (kAct != MOE_ACT_NONE || kGated) unpack8(*reinterpret_cast<const uint4*>(a.z + o), z);
+            if (kGated) unpack8(*reinterpret_cast<const uint4*>(a.u + o), u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (kGated) {
+                    float v, sl;
+                    act_slope<kAct>(z[j], v, sl);
+                    z[j] = d[j] * u[j] * sl;
+                    d[j] *= v;
+                    s0[j] += z[j];
+                    s1[j] += d[j];
+                } else {
+                    if (kAct != MOE_ACT_NONE) {
+                        float v, sl;
+                        act_slope<kAct>(z[j], v, sl);
+                        d[j] *= sl;
+                    }
+                    s0[j] += d[j];
+                }
+            }
+            if (kStore) {
+                if (kGated) {
+                    *reinterpret_cast<uint4*>(a.dz + o) = pack8(z);
+                    *reinterpret_cast<uint4*>(a.dz1 + o) = pack8(d);
+                } else {
+                    *reinterpret_cast<uint4*>(a.dz + o) = pack8(d);
+                }
+            }
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int which = 0; which < (kGated ? 2 : 1); ++which) {
+        float* dst = red[threadIdx.y] + threadIdx.x * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dst[j] = which ? s1[j] : s0[j];
+        __syncthreads();
+        const int cc = threadIdx.y * 32 + threadIdx.x;  // one column per thread
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < kLanes; ++k) v += red[k][cc];
+        const int col = blockIdx.x * kCols + cc;
+        if (col < a.N) a.part[((int64_t)blockIdx.y * (kGated ? 2 : 1) + which) * a.N + col] = v;
+        __syncthreads();
+    }
+}
+
+// out[i] = sum over s < S of part[s * n + i], s in order, 4 per thread.
+template <typename O>
+__global__ void __launch_bounds__(256) sum_splits_kernel(const float* __restrict__ part, int64_t n, int S, int nout,
+                                                         O* out0, O* out1) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < S; ++s) {
+        const float4 p = *reinterpret_cast<const float4*>(part + ((int64_t)s * nout + blockIdx.y) * n + i);
+        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+    }
+    O* out = blockIdx.y ? out1 : out0;
+    if constexpr (sizeof(O) == 4) {
+        *reinterpret_cast<float4*>(out + i) = v;
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(out + i) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+}
+
+}  // namespace
+
+// Row ranges: enough blocks to fill the GPU about 8 times over (2048 threads
+// of an SM hold 8 blocks), each of at least 8 rows.
+int dense_dz_row_blocks(int64_t T, int64_t N) {
+    const int64_t cb = (N + kCols - 1) / kCols;
+    const int64_t want = std::max<int64_t>(1, (8 * 148 + cb - 1) / cb);
+    return (int)std::min<int64_t>(want, std::max<int64_t>(1, (T + kLanes - 1) / kLanes));
+}
+
+cudaError_t launch_dense_dz(DenseDzArgs a, bool gated, int act, float* db0, float* db1, cudaStream_t st) {
+    const int rb = dense_dz_row_blocks(a.T, a.N);
+    a.rows_per_block = (a.T + rb - 1) / rb;
+    const bool store = a.dz != nullptr;
+    if (!(db0 || db1)) a.part = nullptr;
+    const dim3 grid((a.N + kCols - 1) / kCols, rb), block(32, kLanes);
+    trace_before(gated ? "gated_dgu" : "linear_dz", st);
+    by_act(act, [&](auto k) {
+        if (gated)
+            dense_dz_kernel<k.value, true, true><<<grid, block, 0, st>>>(a);
+        else if (store)
+            dense_dz_kernel<k.value, false, true><<<grid, block, 0, st>>>(a);
+        else
+            dense_dz_kernel<MOE_ACT_NONE, false, false><<<grid, block, 0, st>>>(a);
+    });
+    trace_after(st);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.part) return e;
+    const int per = gated ? 2 : 1;
+    return launch_sum_partials(a.part, (int64_t)per * a.N, rb, a.N, a.N, db0, gated ? db1 : nullptr, st);
+}
+
+cudaError_t launch_sum_splits(const float* part, int64_t n, int S, void* out0, void* out1, bool f32,
+                              cudaStream_t st) {
+    const int nout = out1 ? 2 : 1;
+    const dim3 grid((unsigned)((n / 4 + 255) / 256), nout);
+    trace_before("sum_splits", st);
+    if (f32)
+        sum_splits_kernel<float><<<grid, 256, 0, st>>>(part, n, S, nout, (float*)out0, (float*)out1);
+    else
+        sum_splits_kernel<bf16><<<grid, 256, 0, st>>>(part, n, S, nout, (bf16*)out0, (bf16*)out1);
+    trace_after(st);
+    return cudaGetLastError();
+}
+
+}  // namespace moe

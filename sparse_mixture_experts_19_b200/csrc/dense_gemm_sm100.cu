@@ -1,0 +1,614 @@
+// Matrix products of the linear layer and the gate/up projections on the
+// 5th-generation tensor cores (tcgen05, sm_100a), for many rows: forward with
+// a fused epilogue, input gradient and weight gradient.
+//
+//   linear forward  y = act(x W^T + b) + res        A = x,  B = W   (both K-major)
+//   gated forward   h = act(x Wg^T + bg) (x Wu^T + bu): each tile's MMA covers
+//                   128 gate and the 128 matching up columns, so both
+//                   pre-activations of an element meet in one epilogue thread
+//   input gradient  dx = dz W (+ dz' W')            A = dz K-major, B = W read MN-major;
+//                   the gated pair is one reduction over both (two segments)
+//   weight gradient dW = dz^T x (two problems for the gated pair): both MN-major
+//
+// One persistent kernel template on CTA pairs (cta_group::2): a tile is 256
+// rows x kBN columns, each CTA of the pair stages its own 128 rows of A and
+// half of B, and the leader issues M = 256 MMAs that read both CTAs' shared
+// memory: per CTA and 64-deep reduction step 32 KB arrive for 2 x 128 x 256 x
+// 64 flops, which keeps operand traffic below the tensor pipe's time.  TMEM
+// holds two accumulators, so a tile's epilogue overlaps the next tile's main
+// loop.  Bound by the tensor pipe at large sizes, by the stores (weight
+// gradients of few tokens) or the operands' HBM reads otherwise.
+//
+// Roles (10 warps): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
+// epilogue: warp w drains TMEM lanes 32 (w % 4) and one half of the columns.
+// An epilogue warp stages 32 rows x 128 bytes in shared memory (128-byte
+// swizzle) and stores it by TMA, which clips the ragged edges; the residual
+// tile arrives by TMA in the same buffers before the accumulator is ready.
+// Every wait is bounded; a timeout sets MOE_DEVFLAG_WAIT_TIMEOUT and the CTA
+// unwinds.  No multicast loads.
+#include <algorithm>
+
+#include "act.cuh"
+#include "dense.cuh"
+#include "dense_gemm.cuh"
+#include "sm100.cuh"
+#include "tma_host.cuh"
+
+namespace moe {
+namespace {
+
+using namespace sm100;
+
+constexpr int kBM = 128;  // rows per CTA (256 per pair)
+constexpr int kBK = 64;   // reduction step: one 128-byte swizzle row of bf16
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kAccCols = 256;
+constexpr int kTmemCols = 2 * kAccCols;
+constexpr int kABytes = kBM * kBK * 2;
+constexpr int kBox = 64 * kBK * 2;      // a 64 x 64 box of an MN-major operand
+constexpr int kEpiBuf = 32 * 128;       // 32 rows x 128 bytes
+constexpr int kEpiBytes = kEpiWarps * 2 * kEpiBuf;
+
+// What a tile's epilogue does.
+enum Mode { kLinear = 0, kGated = 1, kF32 = 2 };
+
+template <int kBN, int kMode>
+struct Cfg {
+    static constexpr int kBHalf = kMode == kGated ? 128 : kBN / 2;  // B rows each CTA stages
+    static constexpr int kMmaN = 2 * kBHalf;
+    static constexpr int kBBytes = kBHalf * kBK * 2;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = kBHalf == 128 ? 5 : 6;
+    static constexpr size_t kEpiOff = (size_t)kStages * kStageBytes;
+    static constexpr size_t kBarOff = kEpiOff + kEpiBytes;
+    static constexpr size_t kSmem = kBarOff + 512 + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+struct Args {
+    int M, N;        // output rows and columns of one problem
+    int mt, nt;      // tiles of 256 rows, kBN columns
+    int gm;          // row tiles per band
+    int seg_steps;   // reduction steps of one segment
+    int steps;       // reduction steps in all (segments x seg_steps)
+    int split_steps; // steps of one split (= steps when there is one)
+    int problems;    // 1 or 2: weight gradients that share B
+    int splits;      // > 1: partial sums to slice split * problems + problem of D0
+    int64_t total;
+    int act;
+    const float* bias0;
+    const float* bias1;
+    bool has_res, has_z0, has_z1;
+    int32_t* flags;
+};
+
+struct Tile {
+    int m0, n0, prob, split, k0, k1;
+};
+
+// Tiles of one problem and split: bands of gm row tiles, the row tile running
+// fastest, so that pairs working side by side share B's columns and a band's A
+// rows stay in L2.
+template <int kBN>
+__device__ __forceinline__ Tile decode(int64_t t, const Args& a) {
+    const int per = a.mt * a.nt;
+    const int z = (int)(t / per), local = (int)(t % per);
+    const int band = local / (a.gm * a.nt), rem = local - band * a.gm * a.nt;
+    const int first = band * a.gm, width = min(a.gm, a.mt - first);
+    Tile ti;
+    ti.prob = z % a.problems;
+    ti.split = z / a.problems;
+    ti.n0 = rem / width * kBN;
+    ti.m0 = (first + rem % width) * (2 * kBM);
+    ti.k0 = ti.split * a.split_steps;
+    ti.k1 = min(ti.k0 + a.split_steps, a.steps);
+    return ti;
+}
+
+__device__ __forceinline__ uint32_t buf_off(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void pack32(const float (&v)[32], uint32_t* o) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = pack2(v[2 * i], v[2 * i + 1]);
+}
+
+// v[i] += bias[n + i]; the columns past N (a multiple of 8) are not read.
+__device__ __forceinline__ void add_bias(float (&v)[32], const float* bias, int n, int N) {
+    if (!bias) return;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4)
+        if (n + i < N) {
+            const float4 b = __ldg(reinterpret_cast<const float4*>(bias + n + i));
+            v[i] += b.x, v[i + 1] += b.y, v[i + 2] += b.z, v[i + 3] += b.w;
+        }
+}
+
+// 16 packed words into row `lane` of a staging buffer, columns 32 * sub on.
+__device__ __forceinline__ void stage16(uint32_t buf, int lane, int sub, const uint32_t* o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        st_shared_u4(buf + buf_off(lane, 4 * sub + i), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+}
+
+// The warp's staged buffer -> the map's box at (col, row, depth).
+__device__ __forceinline__ void store_buf(const CUtensorMap* map, uint32_t buf, int lane, int col, int row, int depth) {
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_3d(map, buf, col, row, depth);
+        bulk_commit();
+    }
+}
+
+template <int kLeft>
+__device__ __forceinline__ void buffers_free(int lane) {
+    if (lane == 0) bulk_wait_read<kLeft>();
+    __syncwarp();
+}
+
+template <int kBN, int kMode, bool kAMN, bool kBMN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_gemm_kernel(
+    const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mA1,
+    const __grid_constant__ CUtensorMap mB0, const __grid_constant__ CUtensorMap mB1,
+    const __grid_constant__ CUtensorMap mD0, const __grid_constant__ CUtensorMap mD1,
+    const __grid_constant__ CUtensorMap mD2, const __grid_constant__ CUtensorMap mR, const Args a) {
+    using C = Cfg<kBN, kMode>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // used in the leader
+    uint64_t* empty = full + C::kStages;
+    uint64_t* tfull = empty + C::kStages;
+    uint64_t* tempty = tfull + 2;  // used in the leader: 8 epilogue warps x 2 CTAs
+    uint64_t* drain = tempty + 2;
+    uint64_t* rbar = drain + 1;  // residual: 2 buffers x 8 warps
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(rbar + 2 * kEpiWarps);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 2 * kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&rbar[i], 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_holder, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    const int64_t pair = blockIdx.x / 2, npairs = gridDim.x / 2;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer (both CTAs)
+        if (lane == 0) {
+            tma_prefetch_map(&mA0);
+            tma_prefetch_map(&mB0);
+            uint32_t it = 0;
+            for (int64_t t = pair; t < a.total && !*abort_flag; t += npairs) {
+                const Tile ti = decode<kBN>(t, a);
+                const int arow = ti.m0 + (int)rank * kBM;
+                const int brow = kMode == kGated ? ti.n0 : ti.n0 + (int)rank * C::kBHalf;
+                for (int ks = ti.k0; ks < ti.k1; ++ks, ++it) {
+                    const int s = it % C::kStages;
+                    if (!wait_or_abort(&empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag, a.flags)) break;
+                    const bool seg1 = ks >= a.seg_steps;
+                    const int kc = (seg1 ? ks - a.seg_steps : ks) * kBK;
+                    const CUtensorMap* pA = seg1 || ti.prob ? &mA1 : &mA0;
+                    const CUtensorMap* pB = seg1 || (kMode == kGated && rank) ? &mB1 : &mB0;
+                    uint8_t* sa = smem + s * C::kStageBytes;
+                    uint8_t* sb = sa + kABytes;
+                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+                    if (kAMN) {
+                        tma_load_3d_pair(sa, pA, &full[s], arow, kc, 0);
+                        tma_load_3d_pair(sa + kBox, pA, &full[s], arow + 64, kc, 0);
+                    } else {
+                        tma_load_3d_pair(sa, pA, &full[s], kc, arow, 0);
+                    }
+                    if (kBMN) {
+#pragma unroll
+                        for (int j = 0; j < C::kBHalf / 64; ++j)
+                            tma_load_3d_pair(sb + j * kBox, pB, &full[s], brow + 64 * j, kc, 0);
+                    } else {
+                        tma_load_3d_pair(sb, pB, &full[s], kc, brow, 0);
+                    }
+                }
+            }
+            // copies of both CTAs complete on the leader's barriers
+            if (leader)
+                for (uint32_t j = (it > (uint32_t)C::kStages ? it - C::kStages : 0); j < it; ++j)
+                    drain_wait(&full[j % C::kStages], (j / C::kStages) & 1);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (leader)
+        if (lane == 0 && leader) {
+            constexpr uint32_t kIdesc = idesc_bf16_major(2 * kBM, C::kMmaN, kAMN, kBMN);
+            uint32_t it = 0, tc = 0;
+            for (int64_t t = pair; t < a.total && !*abort_flag; t += npairs, ++tc) {
+                const Tile ti = decode<kBN>(t, a);
+                const uint32_t acc = tc & 1;
+                if (!wait_or_abort(&tempty[acc], ((tc >> 1) & 1) ^ 1, abort_flag, a.flags)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + acc * kAccCols;
+                bool ok = true;
+                for (int ks = ti.k0; ks < ti.k1; ++ks, ++it) {
+                    const int s = it % C::kStages;
+                    if (!wait_or_abort(&full[s], (it / C::kStages) & 1, abort_flag, a.flags)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(smem + s * C::kStageBytes), b0 = a0 + kABytes;
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk) {
+                        const uint64_t da = kAMN ? desc_mnmajor_sw128(a0 + kk * 2048, kBox, 1024)
+                                                 : desc_kmajor_sw128(a0 + kk * 32);
+                        const uint64_t db = kBMN ? desc_mnmajor_sw128(b0 + kk * 2048, kBox, 1024)
+                                                 : desc_kmajor_sw128(b0 + kk * 32);
+                        mma_bf16_pair(d, da, db, kIdesc, ks > ti.k0 || kk > 0);
+                    }
+                    mma_commit_pair(&empty[s], 0x3);  // frees the stage in both CTAs
+                }
+                if (!ok) break;
+                mma_commit_pair(&tfull[acc], 0x3);
+            }
+            mma_commit_pair(drain, 0x1);
+            drain_wait(drain, 0);
+        }
+    } else {
+        // ------------------------------------------------ epilogue (both CTAs)
+        const int e = warp - 2, q = warp & 3, half = e >> 2;
+        const uint32_t buf0 = smem_u32(smem + C::kEpiOff) + (uint32_t)e * 2 * kEpiBuf;
+        constexpr int kHalfCols = (kMode == kGated ? 128 : kBN) / 2;  // output columns of this warp
+        constexpr int kChunk = kMode == kF32 ? 32 : 64;               // columns of one staging buffer
+        constexpr int kChunks = kHalfCols / kChunk;
+        uint32_t tc = 0, rph = 0, nb = 0;  // rph bit j: phase of residual buffer j
+        for (int64_t t = pair; t < a.total; t += npairs, ++tc) {
+            const Tile ti = decode<kBN>(t, a);
+            const uint32_t acc = tc & 1;
+            const int row = ti.m0 + (int)rank * kBM + q * 32;
+            const int col0 = ti.n0 + half * kHalfCols;
+            const bool rows_in = row < a.M;
+            if (kMode == kLinear && a.has_res && rows_in) {
+                // the residual chunks into the staging buffers, ahead of the accumulator
+                buffers_free<0>(lane);
+                if (lane == 0)
+#pragma unroll
+                    for (int j = 0; j < kChunks; ++j)
+                        if (col0 + j * kChunk < a.N) {
+                            mbar_arrive_expect_tx(&rbar[2 * e + j], kEpiBuf);
+                            tma_load_3d(smem + C::kEpiOff + (e * 2 + j) * kEpiBuf, &mR, &rbar[2 * e + j],
+                                        col0 + j * kChunk, row, 0);
+                        }
+            }
+            const bool ok = wait_sleep_or_abort(&tfull[acc], (tc >> 1) & 1, abort_flag, a.flags);
+            if (!ok) {
+                if (kMode == kLinear && a.has_res && rows_in)
+                    for (int j = 0; j < kChunks; ++j)
+                        if (col0 + j * kChunk < a.N) drain_wait(&rbar[2 * e + j], (rph >> j) & 1);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t tq = tmem_base + acc * kAccCols + ((uint32_t)(q * 32) << 16) + half * kHalfCols;
+            if (kMode == kF32) {
+#pragma unroll 1
+                for (int j = 0; j < kChunks; ++j) {
+                    float v[32];
+                    tmem_ld32(tq + j * 32, v);
+                    if (j == kChunks - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(&tempty[acc], 0);
+                    }
+                    const int col = col0 + j * 32;
+                    if (!rows_in || col >= a.N) continue;
+                    const uint32_t buf = buf0 + (nb++ & 1) * kEpiBuf;
+                    buffers_free<1>(lane);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        st_shared_u4(buf + buf_off(lane, i), __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                     __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+                    const bool parts = a.splits > 1;
+                    store_buf(!parts && ti.prob ? &mD1 : &mD0, buf, lane, col, row,
+                              parts ? ti.split * a.problems + ti.prob : 0);
+                }
+            } else if (kMode == kGated) {
+                uint32_t h[32];
+                const int col = col0;
+                const bool live = rows_in && col < a.N;
+                const bool keep = a.has_z0 || a.has_z1;
+                if (live && keep) buffers_free<0>(lane);
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub) {
+                    float g[32], u[32];
+                    tmem_ld32(tq + 32 * sub, g);
+                    tmem_ld32(tq + 128 + 32 * sub, u);
+                    if (sub == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(&tempty[acc], 0);
+                    }
+                    if (!live) continue;
+                    add_bias(g, a.bias0, col + 32 * sub, a.N);
+                    add_bias(u, a.bias1, col + 32 * sub, a.N);
+                    uint32_t o[16];
+                    if (a.has_z0) {
+                        pack32(g, o);
+                        stage16(buf0, lane, sub, o);
+                    }
+                    if (a.has_z1) {
+                        pack32(u, o);
+                        stage16(buf0 + kEpiBuf, lane, sub, o);
+                    }
+                    by_act(a.act, [&](auto k) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) g[i] = act_value<k.value>(g[i]) * u[i];
+                    });
+                    pack32(g, h + 16 * sub);
+                }
+                if (live) {
+                    if (a.has_z0) store_buf(&mD1, buf0, lane, col, row, 0);
+                    if (a.has_z1) store_buf(&mD2, buf0 + kEpiBuf, lane, col, row, 0);
+                    const uint32_t buf = buf0 + (keep ? 0 : nb & 1) * kEpiBuf;
+                    if (a.has_z0 && a.has_z1)
+                        buffers_free<1>(lane);  // g's store has read buffer 0
+                    else if (keep)
+                        buffers_free<0>(lane);
+                    else
+                        buffers_free<1>(lane);
+                    ++nb;
+                    stage16(buf, lane, 0, h);
+                    stage16(buf, lane, 1, h + 16);
+                    store_buf(&mD0, buf, lane, col, row, 0);
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < kChunks; ++j) {
+                    const int col = col0 + j * kChunk;
+                    const bool live = rows_in && col < a.N;
+                    const bool z = a.has_z0, res = a.has_res;
+                    // with a residual the chunk's buffer is the one it arrived in
+                    const uint32_t buf = buf0 + (res ? j : nb & 1) * kEpiBuf;
+                    if (live) {
+                        if (res) {
+                            const bool got = wait_or_abort(&rbar[2 * e + j], (rph >> j) & 1, abort_flag, a.flags);
+                            if (!got) drain_wait(&rbar[2 * e + j], (rph >> j) & 1);
+                            rph ^= 1u << j;
+                        } else {
+                            buffers_free<1>(lane);
+                        }
+                    }
+                    uint32_t y[32];
+#pragma unroll
+                    for (int sub = 0; sub < 2; ++sub) {
+                        float v[32];
+                        tmem_ld32(tq + j * kChunk + 32 * sub, v);
+                        if (j == kChunks - 1 && sub == 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(&tempty[acc], 0);
+                        }
+                        if (!live) continue;
+                        add_bias(v, a.bias0, col + 32 * sub, a.N);
+                        uint32_t r[16];
+                        if (res)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 w = ld_shared_u4(buf + buf_off(lane, 4 * sub + i));
+                                r[4 * i] = w.x, r[4 * i + 1] = w.y, r[4 * i + 2] = w.z, r[4 * i + 3] = w.w;
+                            }
+                        if (z) {
+                            uint32_t o[16];
+                            pack32(v, o);
+                            stage16(buf, lane, sub, o);
+                        }
+                        by_act(a.act, [&](auto k) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = act_value<k.value>(v[i]);
+                        });
+                        if (res)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                v[2 * i] += __uint_as_float(r[i] << 16);
+                                v[2 * i + 1] += __uint_as_float(r[i] & 0xffff0000u);
+                            }
+                        pack32(v, y + 16 * sub);
+                    }
+                    if (live) {
+                        if (z) {
+                            store_buf(&mD1, buf, lane, col, row, 0);
+                            buffers_free<0>(lane);
+                        }
+                        stage16(buf, lane, 0, y);
+                        stage16(buf, lane, 1, y + 16);
+                        const bool second = ti.prob != 0;
+                        store_buf(second ? &mD1 : &mD0, buf, lane, col, row, 0);
+                        ++nb;
+                    }
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+
+    __syncwarp();  // the single-lane roles join their warps
+    if (*abort_flag && !leader) {
+        // aborted: this CTA's copies complete on the leader's barriers; give
+        // any still in flight time to land before shared memory is released
+        for (int i = 0; i < 2000; ++i) __nanosleep(100);
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
+}
+
+struct Maps {
+    CUtensorMap A0, A1, B0, B1, D0, D1, D2, R;
+};
+
+template <int kBN, int kMode, bool kAMN, bool kBMN>
+cudaError_t launch(const Maps& m, Args a, const char* name, cudaStream_t st) {
+    using C = Cfg<kBN, kMode>;
+    auto* fn = dense_gemm_kernel<kBN, kMode, kAMN, kBMN>;
+    cudaError_t e = ensure_smem_attr(fn, C::kSmem);
+    if (e != cudaSuccess) return e;
+    const int pairs = device_sm_count() / 2;
+    const int grid = 2 * (int)std::max<int64_t>(1, std::min<int64_t>(pairs, a.total));
+    trace_before(name, st);
+    fn<<<grid, kThreads, C::kSmem, st>>>(m.A0, m.A1, m.B0, m.B1, m.D0, m.D1, m.D2, m.R, a);
+    trace_after(st);
+    return cudaGetLastError();
+}
+
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Row tiles per band: A rows of about 32 MB.
+int band_of(int64_t k) {
+    const int64_t g = (32ll << 20) / (2 * kBM * 2 * std::max<int64_t>(k, 1));
+    return (int)std::min<int64_t>(std::max<int64_t>(g, 8), 1 << 20);
+}
+
+// Column tile: 256, or 128 when its finer grid leaves fewer idle pairs in the
+// last wave by more than the 6% that its larger operand traffic costs.
+bool narrow_tiles(int64_t M, int64_t N, int64_t copies) {
+    const int64_t pairs = kDensePairs, mt = cdiv(M, 2 * kBM) * copies;
+    const double wide = (double)((mt * cdiv(N, 256) + pairs - 1) / pairs) * 2;
+    const double narrow = (double)((mt * cdiv(N, 128) + pairs - 1) / pairs) * 1.06;
+    return narrow < wide;
+}
+
+void fill(Args& a, int64_t M, int N, int bn, int64_t k, int segs, int32_t* flags) {
+    a.M = (int)M;
+    a.N = N;
+    a.mt = cdiv(M, 2 * kBM);
+    a.nt = cdiv(N, bn);
+    a.gm = band_of(k * segs);
+    a.seg_steps = cdiv(k, kBK);
+    a.steps = a.seg_steps * segs;
+    a.split_steps = a.steps;
+    a.problems = a.splits = 1;
+    a.total = (int64_t)a.mt * a.nt;
+    a.flags = flags;
+}
+
+}  // namespace
+
+cudaError_t launch_dense_fwd_pairs(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
+                                   const DenseOut& o, int32_t* flags, cudaStream_t st) {
+    const bool gated = w1 != nullptr;
+    const bool narrow = !gated && narrow_tiles(T, N, 1);
+    const int bn = gated || narrow ? 128 : 256;
+    const int bhalf = narrow ? 64 : 128;
+    Maps m;
+    bool ok = make_tile_map(&m.A0, false, x, K, T, 1, kBM) && make_tile_map(&m.B0, false, w0, K, N, 1, bhalf) &&
+              make_tile_map(&m.D0, false, o.y, N, T, 1, 32);
+    m.A1 = m.A0;
+    m.B1 = m.B0;
+    m.D1 = m.D2 = m.R = m.D0;
+    if (gated) ok = ok && make_tile_map(&m.B1, false, w1, K, N, 1, bhalf);
+    if (o.z0) ok = ok && make_tile_map(&m.D1, false, o.z0, N, T, 1, 32);
+    if (o.z1) ok = ok && make_tile_map(&m.D2, false, o.z1, N, T, 1, 32);
+    if (o.res) ok = ok && make_tile_map(&m.R, false, o.res, N, T, 1, 32);
+    if (!ok) return cudaErrorInvalidValue;
+    Args a{};
+    fill(a, T, N, bn, K, 1, flags);
+    a.act = o.act;
+    a.bias0 = o.bias0;
+    a.bias1 = o.bias1;
+    a.has_res = o.res != nullptr;
+    a.has_z0 = o.z0 != nullptr;
+    a.has_z1 = o.z1 != nullptr;
+    if (gated) return launch<128, kGated, false, false>(m, a, "gated_fwd", st);
+    if (narrow) return launch<128, kLinear, false, false>(m, a, "linear_fwd", st);
+    return launch<256, kLinear, false, false>(m, a, "linear_fwd", st);
+}
+
+cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T,
+                                     int K, int N, void* dx, int32_t* flags, cudaStream_t st) {
+    const bool narrow = narrow_tiles(T, K, 1);
+    Maps m;
+    bool ok = make_tile_map(&m.A0, false, dz0, N, T, 1, kBM) && make_tile_map(&m.B0, false, w0, K, N, 1, 64) &&
+              make_tile_map(&m.D0, false, dx, K, T, 1, 32);
+    m.A1 = m.A0;
+    m.B1 = m.B0;
+    m.D1 = m.D2 = m.R = m.D0;
+    if (dz1)
+        ok = ok && make_tile_map(&m.A1, false, dz1, N, T, 1, kBM) && make_tile_map(&m.B1, false, w1, K, N, 1, 64);
+    if (!ok) return cudaErrorInvalidValue;
+    Args a{};
+    fill(a, T, K, narrow ? 128 : 256, N, dz1 ? 2 : 1, flags);
+    const char* name = dz1 ? "gated_dgrad" : "linear_dgrad";
+    if (narrow) return launch<128, kLinear, false, true>(m, a, name, st);
+    return launch<256, kLinear, false, true>(m, a, name, st);
+}
+
+// Splits of the weight gradient's reduction (the tokens): as many as fill the
+// pairs when the output has few tiles, each of at least 16 steps (1024 tokens).
+static int wgrad_splits(int64_t T, int K, int N, int problems) {
+    const int64_t tiles = (int64_t)cdiv(N, 256) * cdiv(K, 256) * problems;
+    const int64_t steps = cdiv(T, kBK);
+    const int64_t s = std::min<int64_t>(kDensePairs / tiles, steps / 16);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(s, 16));
+}
+
+size_t dense_wgrad_part_floats(int64_t T, int K, int N, int problems) {
+    const int s = wgrad_splits(T, K, N, problems);
+    return s > 1 ? (size_t)s * problems * N * K : 0;
+}
+
+cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, int64_t T, int K, int N, void* dw0,
+                               void* dw1, bool f32, float* part, int32_t* flags, cudaStream_t st) {
+    const int problems = dz1 ? 2 : 1;
+    const int splits = wgrad_splits(T, K, N, problems);
+    const bool parts = splits > 1;
+    const bool out32 = f32 || parts;
+    Maps m;
+    bool ok = make_tile_map(&m.A0, false, dz0, N, T, 1, 64) && make_tile_map(&m.B0, false, x, K, T, 1, 64);
+    if (parts)
+        ok = ok && make_tile_map(&m.D0, true, part, K, N, (uint64_t)splits * problems, 32);
+    else
+        ok = ok && make_tile_map(&m.D0, f32, dw0, K, N, 1, 32);
+    m.A1 = m.A0;
+    m.B1 = m.B0;
+    m.D1 = m.D2 = m.R = m.D0;
+    if (dz1) {
+        ok = ok && make_tile_map(&m.A1, false, dz1, N, T, 1, 64);
+        if (!parts) ok = ok && make_tile_map(&m.D1, f32, dw1, K, N, 1, 32);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    const bool narrow = !parts && narrow_tiles(N, K, problems);
+    Args a{};
+    fill(a, N, K, narrow ? 128 : 256, T, 1, flags);
+    a.problems = problems;
+    a.splits = splits;
+    a.split_steps = cdiv(a.steps, splits);
+    a.total *= (int64_t)problems * splits;
+    const char* name = dz1 ? "gated_wgrad" : "linear_wgrad";
+    cudaError_t e;
+    if (out32)
+        e = narrow ? launch<128, kF32, true, true>(m, a, name, st) : launch<256, kF32, true, true>(m, a, name, st);
+    else
+        e = narrow ? launch<128, kLinear, true, true>(m, a, name, st) : launch<256, kLinear, true, true>(m, a, name, st);
+    if (e != cudaSuccess || !parts) return e;
+    return launch_sum_splits(part, (int64_t)N * K, splits, dw0, dw1, f32, st);
+}
+
+}  // namespace moe

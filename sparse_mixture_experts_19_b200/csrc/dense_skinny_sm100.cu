@@ -1,0 +1,347 @@
+// Matrix products of the linear layer and the gate/up projections for few
+// rows (sm_100a): forward and input gradient where the weights' stream from
+// HBM is the bound.
+//
+// The weights take the tensor core's 128-row side and the tokens its column
+// side: D[128 output features][kTN tokens], so a call of one token wastes 15
+// columns of a cheap MMA instead of 255 rows, and every SM spends its time on
+// weight bytes.  A CTA owns one tile and one share of the reduction: a cluster
+// of S <= 8 CTAs splits the reduction (enough clusters to cover the SMs when
+// the output has few feature tiles), each streams its share through a TMA ring
+// of up to 200 KB (weights 16 KB per 64-deep step, read once), and the S
+// partial tiles are added through distributed shared memory in rank order:
+// CTA r finishes the r-th share of the tokens.  The sum's order depends on the
+// sizes alone, so the bits do not change from run to run.
+//
+//   forward: A = W rows K-major; gated: two A tiles (gate, up) and two
+//            accumulators per step
+//   input gradient: A = W read MN-major (features = W's columns), B = dz; the
+//            gated pair is one reduction over both (two segments)
+//
+// Six warps: TMA producer, MMA issuer, four that move the accumulator from
+// TMEM to shared memory; then all of them finish the elements (bias,
+// activation, residual).  Waits are bounded; no multicast loads.
+#include <algorithm>
+
+#include "act.cuh"
+#include "dense.cuh"
+#include "dense_gemm.cuh"
+#include "sm100.cuh"
+#include "tma_host.cuh"
+
+namespace moe {
+namespace {
+
+using namespace sm100;
+
+constexpr int kBK = 64;
+constexpr int kThreads = 192;
+constexpr int kABytes = 128 * kBK * 2;
+constexpr int kBox = 64 * kBK * 2;
+constexpr int kMaxStages = 12;
+constexpr int kRingBytes = 208 * 1024;
+constexpr size_t kSmem = kRingBytes + 512 + 1024;
+
+struct Args {
+    int T, N;        // tokens, output features
+    int tn;          // tokens per tile (multiple of 16)
+    int stages;
+    int seg_steps, steps;
+    int splits;      // CTAs per cluster
+    int act;
+    const float* bias0;
+    const float* bias1;
+    const bf16* res;
+    bf16* y;
+    bf16* z0;
+    bf16* z1;
+    uint32_t tmem_cols;
+    int32_t* flags;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store4(bf16* p, const float (&v)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+template <bool kGated, bool kAMN>
+__global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_constant__ CUtensorMap mA0,
+                                                                   const __grid_constant__ CUtensorMap mA1,
+                                                                   const __grid_constant__ CUtensorMap mB0,
+                                                                   const __grid_constant__ CUtensorMap mB1,
+                                                                   const Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes);
+    uint64_t* empty = full + kMaxStages;
+    uint64_t* done = empty + kMaxStages;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = a.splits > 1 ? cluster_ctarank() : 0;
+    const int n0 = (int)(blockIdx.x / a.splits) * 128, t0 = (int)blockIdx.y * a.tn;
+    const int ks0 = (int)((int64_t)a.steps * rank / a.splits), ks1 = (int)((int64_t)a.steps * (rank + 1) / a.splits);
+    const int b_bytes = a.tn * kBK * 2;
+    const int stage_bytes = (kGated ? 2 : 1) * kABytes + b_bytes;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, a.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 1;
+            int it = 0;
+            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                if (!wait_or_abort(&empty[s], ph, abort_flag, a.flags)) break;
+                const bool seg1 = ks >= a.seg_steps;
+                const int kc = (seg1 ? ks - a.seg_steps : ks) * kBK;
+                uint8_t* sa = smem + s * stage_bytes;
+                uint8_t* sb = sa + (kGated ? 2 : 1) * kABytes;
+                mbar_arrive_expect_tx(&full[s], stage_bytes);
+                if (kAMN) {
+                    const CUtensorMap* pA = seg1 ? &mA1 : &mA0;
+                    tma_load_3d(sa, pA, &full[s], n0, kc, 0);
+                    tma_load_3d(sa + kBox, pA, &full[s], n0 + 64, kc, 0);
+                } else {
+                    tma_load_3d(sa, &mA0, &full[s], kc, n0, 0);
+                    if (kGated) tma_load_3d(sa + kABytes, &mA1, &full[s], kc, n0, 0);
+                }
+                tma_load_3d(sb, seg1 ? &mB1 : &mB0, &full[s], kc, t0, 0);
+                if (++s == a.stages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            // every copy has landed before the ring is reused or released
+            for (int j = std::max(0, it - a.stages); j < it; ++j) drain_wait(&full[j % a.stages], (j / a.stages) & 1);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16_major(128, a.tn, kAMN, false);
+            int s = 0;
+            uint32_t ph = 0;
+            for (int ks = ks0; ks < ks1; ++ks) {
+                if (!wait_or_abort(&full[s], ph, abort_flag, a.flags)) break;
+                tc_fence_after();
+                const uint32_t a0 = smem_u32(smem + s * stage_bytes), b0 = a0 + (kGated ? 2 : 1) * kABytes;
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk) {
+                    const uint64_t da =
+                        kAMN ? desc_mnmajor_sw128(a0 + kk * 2048, kBox, 1024) : desc_kmajor_sw128(a0 + kk * 32);
+                    const uint64_t db = desc_kmajor_sw128(b0 + kk * 32);
+                    mma_bf16(tmem_base, da, db, idesc, ks > ks0 || kk > 0);
+                    if (kGated)
+                        mma_bf16(tmem_base + a.tn, desc_kmajor_sw128(a0 + kABytes + kk * 32), db, idesc,
+                                 ks > ks0 || kk > 0);
+                }
+                mma_commit(&empty[s]);
+                if (++s == a.stages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            mma_commit(done);
+            drain_wait(done, 0);
+        }
+    } else {
+        // ------------------------------------------------ TMEM -> partial tile in shared memory
+        // (the ring is free: the accumulator is complete, so every step's
+        // operands have been read).  part[acc][token][128 features]
+        const int q = warp & 3;
+        const bool ok = wait_sleep_or_abort(done, 0, abort_flag, a.flags);
+        tc_fence_after();
+        float* part = reinterpret_cast<float*>(smem);
+        const int cols = (kGated ? 2 : 1) * a.tn;
+        if (ok)
+            for (int c = 0; c < cols; c += 16) {
+                float v[16];
+                tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + c, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) part[(c + i) * 128 + q * 32 + lane] = ks1 > ks0 ? v[i] : 0.f;
+            }
+        tc_fence_before();
+    }
+    __syncwarp();  // the single-lane roles join their warps
+    if (a.splits > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+
+    // ---------------------------------------------------- finish: 4 features of a token per thread
+    const int tokens = min(a.tn, a.T - t0);
+    const int tk0 = tokens * (int)rank / a.splits, tk1 = tokens * ((int)rank + 1) / a.splits;
+    const uint32_t base = smem_u32(smem);
+    for (int i = tk0 * 32 + (int)threadIdx.x; i < tk1 * 32; i += kThreads) {
+        const int tok = i / 32, f = (i % 32) * 4, n = n0 + f;
+        if (n >= a.N) continue;  // N is a multiple of 8
+        float v[2][4];
+#pragma unroll
+        for (int p = 0; p < (kGated ? 2 : 1); ++p) {
+            const uint32_t off = base + (uint32_t)(((p * a.tn + tok) * 128 + f) * 4);
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < a.splits; ++r) {
+                const float4 w = ld_cluster_f4(a.splits > 1 ? mapa_shared(off, r) : off);
+                s.x += w.x, s.y += w.y, s.z += w.z, s.w += w.w;
+            }
+            const float* bias = p ? a.bias1 : a.bias0;
+            if (bias) {
+                const float4 b = *reinterpret_cast<const float4*>(bias + n);
+                s.x += b.x, s.y += b.y, s.z += b.z, s.w += b.w;
+            }
+            v[p][0] = s.x, v[p][1] = s.y, v[p][2] = s.z, v[p][3] = s.w;
+        }
+        const int64_t o = (int64_t)(t0 + tok) * a.N + n;
+        if (a.z0) store4(a.z0 + o, v[0]);
+        if (kGated && a.z1) store4(a.z1 + o, v[1]);
+        by_act(a.act, [&](auto k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[0][j] = act_value<k.value>(v[0][j]);
+        });
+        if (kGated)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[0][j] *= v[1][j];
+        if (a.res) {
+            const uint2 w = *reinterpret_cast<const uint2*>(a.res + o);
+            v[0][0] += __uint_as_float(w.x << 16), v[0][1] += __uint_as_float(w.x & 0xffff0000u);
+            v[0][2] += __uint_as_float(w.y << 16), v[0][3] += __uint_as_float(w.y & 0xffff0000u);
+        }
+        store4(a.y + o, v[0]);
+    }
+    if (a.splits > 1)
+        cluster_sync();  // the peers have read this CTA's partial tile
+    else
+        __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, a.tmem_cols);
+}
+
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Tokens per tile and the cluster's size: one token tile up to tn_max tokens,
+// and as many CTAs per tile as keep all of them on the SMs at once, each with
+// at least 4 reduction steps.
+void fill(Args& a, int64_t T, int N, int64_t k, int segs, bool gated, int32_t* flags) {
+    const int tn_max = gated ? 128 : 256;
+    a.T = (int)T;
+    a.N = N;
+    const int tiles_t = cdiv(T, tn_max);
+    a.tn = cdiv(cdiv(T, tiles_t), 16) * 16;
+    a.seg_steps = cdiv(k, kBK);
+    a.steps = a.seg_steps * segs;
+    const int stage = (gated ? 2 : 1) * kABytes + a.tn * kBK * 2;
+    a.stages = std::min(kMaxStages, kRingBytes / stage);
+    const int64_t tiles = (int64_t)cdiv(N, 128) * cdiv(T, a.tn);
+    a.splits = 1;
+    while (a.splits < 8 && tiles * a.splits * 2 <= 2 * kDensePairs && a.steps / (a.splits * 2) >= 4) a.splits *= 2;
+    const uint32_t cols = (gated ? 2 : 1) * a.tn;
+    a.tmem_cols = 32;
+    while (a.tmem_cols < cols) a.tmem_cols *= 2;
+    a.flags = flags;
+}
+
+template <bool kGated, bool kAMN>
+cudaError_t launch(const CUtensorMap& A0, const CUtensorMap& A1, const CUtensorMap& B0, const CUtensorMap& B1,
+                   const Args& a, const char* name, cudaStream_t st) {
+    auto* fn = dense_skinny_kernel<kGated, kAMN>;
+    cudaError_t e = ensure_smem_attr(fn, kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(cdiv(a.N, 128) * a.splits), (unsigned)cdiv(a.T, a.tn), 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    trace_before(name, st);
+    e = cudaLaunchKernelEx(&cfg, fn, A0, A1, B0, B1, a);
+    trace_after(st);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_dense_fwd_skinny(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
+                                    const DenseOut& o, int32_t* flags, cudaStream_t st) {
+    Args a{};
+    fill(a, T, N, K, 1, w1 != nullptr, flags);
+    a.act = o.act;
+    a.bias0 = o.bias0;
+    a.bias1 = o.bias1;
+    a.res = o.res;
+    a.y = o.y;
+    a.z0 = o.z0;
+    a.z1 = o.z1;
+    CUtensorMap A0, A1, B;
+    if (!make_tile_map(&A0, false, w0, K, N, 1, 128) || !make_tile_map(&B, false, x, K, T, 1, a.tn))
+        return cudaErrorInvalidValue;
+    A1 = A0;
+    if (w1 && !make_tile_map(&A1, false, w1, K, N, 1, 128)) return cudaErrorInvalidValue;
+    if (w1) return launch<true, false>(A0, A1, B, B, a, "gated_fwd_skinny", st);
+    return launch<false, false>(A0, A1, B, B, a, "linear_fwd_skinny", st);
+}
+
+cudaError_t launch_dense_dgrad_skinny(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T,
+                                      int K, int N, void* dx, int32_t* flags, cudaStream_t st) {
+    Args a{};
+    fill(a, T, K, N, dz1 ? 2 : 1, false, flags);
+    a.y = static_cast<bf16*>(dx);
+    CUtensorMap A0, A1, B0, B1;
+    if (!make_tile_map(&A0, false, w0, K, N, 1, 64) || !make_tile_map(&B0, false, dz0, N, T, 1, a.tn))
+        return cudaErrorInvalidValue;
+    A1 = A0;
+    B1 = B0;
+    if (dz1 && (!make_tile_map(&A1, false, w1, K, N, 1, 64) || !make_tile_map(&B1, false, dz1, N, T, 1, a.tn)))
+        return cudaErrorInvalidValue;
+    return launch<false, true>(A0, A1, B0, B1, a, dz1 ? "gated_dgrad_skinny" : "linear_dgrad_skinny", st);
+}
+
+// Few rows: the weights are streamed once and the SMs wait for HBM; many rows:
+// the pair kernel's 256-row tiles.
+static bool skinny(int64_t T) { return T <= 256; }
+
+cudaError_t launch_dense_fwd(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
+                             const DenseOut& o, int32_t* flags, cudaStream_t st) {
+    return skinny(T) ? launch_dense_fwd_skinny(x, w0, w1, T, K, N, o, flags, st)
+                     : launch_dense_fwd_pairs(x, w0, w1, T, K, N, o, flags, st);
+}
+
+cudaError_t launch_dense_dgrad(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T, int K,
+                               int N, void* dx, int32_t* flags, cudaStream_t st) {
+    return skinny(T) ? launch_dense_dgrad_skinny(dz0, dz1, w0, w1, T, K, N, dx, flags, st)
+                     : launch_dense_dgrad_pairs(dz0, dz1, w0, w1, T, K, N, dx, flags, st);
+}
+
+}  // namespace moe

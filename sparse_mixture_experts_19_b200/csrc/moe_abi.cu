@@ -9,6 +9,7 @@
 
 #include <vector>
 
+#include "abi_util.cuh"
 #include "common.cuh"
 
 namespace moe {
@@ -16,7 +17,7 @@ namespace moe {
 // ------------------------------------------------------------------ errors
 static thread_local char g_last_error[256] = "";
 
-static moe_status_t fail(moe_status_t st, const char* fmt, ...) {
+moe_status_t fail(moe_status_t st, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
@@ -24,8 +25,19 @@ static moe_status_t fail(moe_status_t st, const char* fmt, ...) {
     return st;
 }
 
-static moe_status_t cuda_fail(cudaError_t e, const char* where) {
+moe_status_t cuda_fail(cudaError_t e, const char* where) {
     return fail(MOE_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+}
+
+moe_status_t read_device_flags(int32_t* flags, cudaStream_t st, int32_t* flags_out) {
+    int32_t v = 0;
+    CUDA_TRY(cudaMemcpyAsync(&v, flags, sizeof(int32_t), cudaMemcpyDeviceToHost, st), "flags read");
+    CUDA_TRY(cudaStreamSynchronize(st), "stream sync");
+    CUDA_TRY(cudaMemsetAsync(flags, 0, sizeof(int32_t), st), "flags clear");
+    CUDA_TRY(cudaStreamSynchronize(st), "stream sync");
+    if (flags_out) *flags_out = v;
+    if (v) return fail(MOE_ERR_DEVICE_CHECK, "device check flags 0x%x", v);
+    return MOE_OK;
 }
 
 // ----------------------------------------------------------------- tracing
@@ -92,8 +104,6 @@ static int64_t capacity_of(const moe_config_t* c) {
     return C < 1.0 ? 1 : (int64_t)C;
 }
 
-static size_t align_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
-
 // Fills the plan; with ws == nullptr only sizes are computed.
 static void make_plan(const moe_config_t* c, void* ws, Plan* p) {
     p->T = c->T;
@@ -155,25 +165,6 @@ static moe_status_t plan_for(const moe_config_t* c, void* ws, size_t ws_bytes, P
     make_plan(c, ws, p);
     return MOE_OK;
 }
-
-static bool aligned16(const void* ptr) { return ((uintptr_t)ptr & 15) == 0; }
-
-#define REQUIRE_PTR(ptr)                                                                    \
-    do {                                                                                    \
-        if (!(ptr)) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", #ptr);                   \
-        if (!aligned16(ptr)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #ptr); \
-    } while (0)
-
-#define OPTIONAL_PTR(ptr)                                                                   \
-    do {                                                                                    \
-        if ((ptr) && !aligned16(ptr)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #ptr); \
-    } while (0)
-
-#define CUDA_TRY(expr, where)                           \
-    do {                                                \
-        cudaError_t e_ = (expr);                        \
-        if (e_ != cudaSuccess) return cuda_fail(e_, where); \
-    } while (0)
 
 static moe_status_t check_shared(const Plan& p, const void* a, const void* b, const void* c) {
     if (p.Is > 0) {
@@ -723,15 +714,7 @@ moe_status_t moe_get_device_status(const moe_config_t* cfg, void* ws, size_t ws_
     Plan p;
     moe_status_t s = plan_for(cfg, ws, ws_bytes, &p);
     if (s != MOE_OK) return s;
-    cudaStream_t st = (cudaStream_t)stream;
-    int32_t flags = 0;
-    CUDA_TRY(cudaMemcpyAsync(&flags, p.flags, sizeof(int32_t), cudaMemcpyDeviceToHost, st), "flags read");
-    CUDA_TRY(cudaStreamSynchronize(st), "stream sync");
-    CUDA_TRY(cudaMemsetAsync(p.flags, 0, sizeof(int32_t), st), "flags clear");
-    CUDA_TRY(cudaStreamSynchronize(st), "stream sync");
-    if (flags_out) *flags_out = flags;
-    if (flags) return fail(MOE_ERR_DEVICE_CHECK, "device check flags 0x%x", flags);
-    return MOE_OK;
+    return read_device_flags(p.flags, (cudaStream_t)stream, flags_out);
 }
 
 const char* moe_status_string(moe_status_t status) {

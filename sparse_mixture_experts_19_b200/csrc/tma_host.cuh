@@ -69,6 +69,24 @@ inline bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint
     return true;
 }
 
+// Rank-3 map of a contiguous bf16 or float32 tensor [depth][rows][inner] with
+// box {128 bytes, box_rows, 1} and the 128-byte swizzle, for loads (elements
+// out of range read as zero) and stores (they are not written).  Encoded anew
+// for each call: nothing is kept.
+inline bool make_tile_map(CUtensorMap* m, bool f32, const void* base, uint64_t inner, uint64_t rows, uint64_t depth,
+                          uint32_t box_rows) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const uint64_t es = f32 ? 4 : 2;
+    cuuint64_t dims[3] = {inner, rows, depth};
+    cuuint64_t strides[2] = {inner * es, inner * rows * es};
+    cuuint32_t box[3] = {(cuuint32_t)(128 / es), box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Rank-3 map of a byte tensor [depth][rows][inner] (inner contiguous, a
 // multiple of 16 bytes) with box {box_inner, box_rows, 1}; box_inner = 128
 // takes the 128-byte swizzle (16-byte chunk c of box row r at c ^ (r % 8)),
