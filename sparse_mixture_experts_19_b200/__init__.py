@@ -443,26 +443,42 @@ def dense_config(T: int, K: int, N: int, act: str = "none", dtype: str = "bf16",
                               _code(_DTYPES, grad_dtype, "grad_dtype"))
 
 
-def _arg(t, name: str, shape: tuple, dtype: int, optional: bool = False):
-    """Device pointer of a contiguous tensor of this shape and MOE_* dtype on
-    the current device (ints pass through as raw pointers)."""
-    import torch
+class _Call:
+    """Argument marshalling of one call: the current device and its stream are
+    looked up once, each tensor's type, shape, layout and device checked."""
 
-    if t is None:
-        if optional:
-            return None
-        raise MoeError(1, f"{name} is None")
-    if isinstance(t, int):
-        return t
-    want = torch.bfloat16 if dtype == MOE_BF16 else torch.float32
-    if t.dtype != want:
-        raise MoeError(1, f"{name} is {t.dtype}, not {want}")
-    if tuple(t.shape) != tuple(shape):
-        raise MoeError(1, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    p = _ptr(t)
-    if t.device.index != torch.cuda.current_device():
-        raise MoeError(1, f"{name} is on {t.device}, not on the current device")
-    return p
+    __slots__ = ("dev", "f32", "bf16")
+
+    def __init__(self):
+        import torch
+
+        self.dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+        self.f32, self.bf16 = torch.float32, torch.bfloat16
+
+    def arg(self, t, name: str, shape: tuple, dtype: int, optional: bool = False):
+        """Device pointer of a contiguous tensor of this shape and MOE_* dtype
+        on the current device (ints pass through as raw pointers)."""
+        if t is None:
+            if optional:
+                return None
+            raise MoeError(1, f"{name} is None")
+        if isinstance(t, int):
+            return t
+        want = self.bf16 if dtype == MOE_BF16 else self.f32
+        if t.dtype is not want:
+            raise MoeError(1, f"{name} is {t.dtype}, not {want}")
+        if t.shape != shape:
+            raise MoeError(1, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        p = _ptr(t)
+        if t.get_device() != self.dev:
+            raise MoeError(1, f"{name} is on {t.device}, not on the current device")
+        return p
+
+    def ws(self, ws):
+        """(pointer, bytes) of a workspace on the current device."""
+        if ws is not None and not isinstance(ws, int) and ws.is_cuda and ws.get_device() != self.dev:
+            raise MoeError(1, f"ws is on {ws.device}, not on the current device")
+        return _ws(ws)
 
 
 def _sized(size_fn, cfg) -> int:
@@ -524,53 +540,63 @@ def gated_backward_workspace(cfg, device="cuda"):
 def moe_norm_forward(cfg, x, weight, bias, y, mean_out=None, rstd_out=None, stream=None):
     """y = norm(x); mean_out, rstd_out [T] float32 keep the statistics."""
     T, H, d = cfg.T, cfg.H, cfg.dtype
-    _check(load().moe_norm_forward(ctypes.byref(cfg), _arg(x, "x", (T, H), d),
-                                   _arg(weight, "weight", (H,), MOE_F32, True),
-                                   _arg(bias, "bias", (H,), MOE_F32, True), _arg(y, "y", (T, H), d),
-                                   _arg(mean_out, "mean_out", (T,), MOE_F32, True),
-                                   _arg(rstd_out, "rstd_out", (T,), MOE_F32, True), _stream(stream)))
+    c = _Call()
+    arg = c.arg
+    _check(load().moe_norm_forward(ctypes.byref(cfg), arg(x, "x", (T, H), d),
+                                   arg(weight, "weight", (H,), MOE_F32, True),
+                                   arg(bias, "bias", (H,), MOE_F32, True), arg(y, "y", (T, H), d),
+                                   arg(mean_out, "mean_out", (T,), MOE_F32, True),
+                                   arg(rstd_out, "rstd_out", (T,), MOE_F32, True), _stream(stream)))
 
 
 def moe_norm_backward(cfg, dy, x, weight, mean, rstd, d_residual, dx, d_weight, d_bias, ws, stream=None):
     """dx (+ d_residual), d_weight and d_bias (each may be None) of the norm."""
     T, H, d = cfg.T, cfg.H, cfg.dtype
-    p, n = _ws(ws)
-    _check(load().moe_norm_backward(ctypes.byref(cfg), _arg(dy, "dy", (T, H), cfg.dy_dtype),
-                                    _arg(x, "x", (T, H), d), _arg(weight, "weight", (H,), MOE_F32, True),
-                                    _arg(mean, "mean", (T,), MOE_F32, True), _arg(rstd, "rstd", (T,), MOE_F32),
-                                    _arg(d_residual, "d_residual", (T, H), d, True), _arg(dx, "dx", (T, H), d),
-                                    _arg(d_weight, "d_weight", (H,), MOE_F32, True),
-                                    _arg(d_bias, "d_bias", (H,), MOE_F32, True), p, n, _stream(stream)))
+    c = _Call()
+    arg = c.arg
+    p, n = c.ws(ws)
+    _check(load().moe_norm_backward(ctypes.byref(cfg), arg(dy, "dy", (T, H), cfg.dy_dtype),
+                                    arg(x, "x", (T, H), d), arg(weight, "weight", (H,), MOE_F32, True),
+                                    arg(mean, "mean", (T,), MOE_F32, True), arg(rstd, "rstd", (T,), MOE_F32),
+                                    arg(d_residual, "d_residual", (T, H), d, True), arg(dx, "dx", (T, H), d),
+                                    arg(d_weight, "d_weight", (H,), MOE_F32, True),
+                                    arg(d_bias, "d_bias", (H,), MOE_F32, True), p, n, _stream(stream)))
 
 
 def moe_linear_forward(cfg, x, w, bias, residual, y, z_out=None, ws=None, stream=None):
     """y = act(x w^T + bias) + residual; z_out keeps the pre-activations."""
     T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
-    _check(load().moe_linear_forward(ctypes.byref(cfg), _arg(x, "x", (T, K), d), _arg(w, "w", (N, K), d),
-                                     _arg(bias, "bias", (N,), MOE_F32, True),
-                                     _arg(residual, "residual", (T, N), d, True), _arg(y, "y", (T, N), d),
-                                     _arg(z_out, "z_out", (T, N), d, True), *_ws(ws), _stream(stream)))
+    c = _Call()
+    arg = c.arg
+    _check(load().moe_linear_forward(ctypes.byref(cfg), arg(x, "x", (T, K), d), arg(w, "w", (N, K), d),
+                                     arg(bias, "bias", (N,), MOE_F32, True),
+                                     arg(residual, "residual", (T, N), d, True), arg(y, "y", (T, N), d),
+                                     arg(z_out, "z_out", (T, N), d, True), *c.ws(ws), _stream(stream)))
 
 
 def moe_linear_backward(cfg, dy, x, w, z, dx, d_w, d_bias, ws=None, stream=None):
     """dx, d_w, d_bias (each may be None) of the linear layer."""
     T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
-    _check(load().moe_linear_backward(ctypes.byref(cfg), _arg(dy, "dy", (T, N), d),
-                                      _arg(x, "x", (T, K), d, d_w is None), _arg(w, "w", (N, K), d, dx is None),
-                                      _arg(z, "z", (T, N), d, True), _arg(dx, "dx", (T, K), d, True),
-                                      _arg(d_w, "d_w", (N, K), cfg.grad_dtype, True),
-                                      _arg(d_bias, "d_bias", (N,), MOE_F32, True), *_ws(ws), _stream(stream)))
+    c = _Call()
+    arg = c.arg
+    _check(load().moe_linear_backward(ctypes.byref(cfg), arg(dy, "dy", (T, N), d),
+                                      arg(x, "x", (T, K), d, d_w is None), arg(w, "w", (N, K), d, dx is None),
+                                      arg(z, "z", (T, N), d, True), arg(dx, "dx", (T, K), d, True),
+                                      arg(d_w, "d_w", (N, K), cfg.grad_dtype, True),
+                                      arg(d_bias, "d_bias", (N,), MOE_F32, True), *c.ws(ws), _stream(stream)))
 
 
 def moe_gated_forward(cfg, x, w_gate, w_up, b_gate, b_up, h, g_out=None, u_out=None, ws=None, stream=None):
     """h = act(x w_gate^T + b_gate) * (x w_up^T + b_up); g_out, u_out keep the
     two projections."""
     T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
-    _check(load().moe_gated_forward(ctypes.byref(cfg), _arg(x, "x", (T, K), d), _arg(w_gate, "w_gate", (N, K), d),
-                                    _arg(w_up, "w_up", (N, K), d), _arg(b_gate, "b_gate", (N,), MOE_F32, True),
-                                    _arg(b_up, "b_up", (N,), MOE_F32, True), _arg(h, "h", (T, N), d),
-                                    _arg(g_out, "g_out", (T, N), d, True), _arg(u_out, "u_out", (T, N), d, True),
-                                    *_ws(ws), _stream(stream)))
+    c = _Call()
+    arg = c.arg
+    _check(load().moe_gated_forward(ctypes.byref(cfg), arg(x, "x", (T, K), d), arg(w_gate, "w_gate", (N, K), d),
+                                    arg(w_up, "w_up", (N, K), d), arg(b_gate, "b_gate", (N,), MOE_F32, True),
+                                    arg(b_up, "b_up", (N,), MOE_F32, True), arg(h, "h", (T, N), d),
+                                    arg(g_out, "g_out", (T, N), d, True), arg(u_out, "u_out", (T, N), d, True),
+                                    *c.ws(ws), _stream(stream)))
 
 
 def moe_gated_backward(cfg, dh, x, w_gate, w_up, g, u, dx, d_w_gate, d_w_up, d_b_gate=None, d_b_up=None, ws=None,
@@ -578,13 +604,15 @@ def moe_gated_backward(cfg, dh, x, w_gate, w_up, g, u, dx, d_w_gate, d_w_up, d_b
     """dx, the two weight gradients and the two bias gradients (each may be
     None) of the gate/up projections."""
     T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
+    c = _Call()
+    arg = c.arg
     no_dw = d_w_gate is None and d_w_up is None
     _check(load().moe_gated_backward(
-        ctypes.byref(cfg), _arg(dh, "dh", (T, N), d), _arg(x, "x", (T, K), d, no_dw),
-        _arg(w_gate, "w_gate", (N, K), d, dx is None), _arg(w_up, "w_up", (N, K), d, dx is None),
-        _arg(g, "g", (T, N), d), _arg(u, "u", (T, N), d), _arg(dx, "dx", (T, K), d, True),
-        _arg(d_w_gate, "d_w_gate", (N, K), cfg.grad_dtype, True), _arg(d_w_up, "d_w_up", (N, K), cfg.grad_dtype, True),
-        _arg(d_b_gate, "d_b_gate", (N,), MOE_F32, True), _arg(d_b_up, "d_b_up", (N,), MOE_F32, True), *_ws(ws),
+        ctypes.byref(cfg), arg(dh, "dh", (T, N), d), arg(x, "x", (T, K), d, no_dw),
+        arg(w_gate, "w_gate", (N, K), d, dx is None), arg(w_up, "w_up", (N, K), d, dx is None),
+        arg(g, "g", (T, N), d), arg(u, "u", (T, N), d), arg(dx, "dx", (T, K), d, True),
+        arg(d_w_gate, "d_w_gate", (N, K), cfg.grad_dtype, True), arg(d_w_up, "d_w_up", (N, K), cfg.grad_dtype, True),
+        arg(d_b_gate, "d_b_gate", (N,), MOE_F32, True), arg(d_b_up, "d_b_up", (N,), MOE_F32, True), *c.ws(ws),
         _stream(stream)))
 
 

@@ -6,11 +6,11 @@
 
 namespace moe {
 
-constexpr int kMaxNormWidth = 16384;  // longest row the norm kernels hold in registers
-// SMs the backward norm's grid is sized for: a constant, so that the number of
+constexpr int kMaxNormWidth = 16384;  // longest row: 512 threads x 32 elements
+// SMs the norms' grid is sized for: a constant, so that the number of
 // partial sums, and with it the bits of dw and db, is a function of the sizes
 // alone.
-constexpr int kNormBwdSms = 148;
+constexpr int kNormSms = 148;
 
 struct NormArgs {
     int64_t T;
@@ -35,7 +35,7 @@ struct NormArgs {
 };
 
 // CTAs (= partial rows) of the backward norm.
-int norm_bwd_blocks(int64_t T, int H);
+int norm_bwd_blocks(int64_t T);
 cudaError_t launch_norm_fwd(const NormArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormArgs& a, bool f32, bool dy_f32, cudaStream_t st);
 // out0[c] = sum over p < P of part[p * stride + c]; out1 (when non-null) the

@@ -27,7 +27,7 @@ moe_status_t check_norm(const moe_norm_config_t* c) {
 }
 
 size_t norm_ws_bytes(const moe_norm_config_t* c) {
-    return align_up(sizeof(float) * 2 * c->H * (c->T > 0 ? norm_bwd_blocks(c->T, c->H) : 1));
+    return align_up(sizeof(float) * 2 * c->H * (c->T > 0 ? norm_bwd_blocks(c->T) : 1));
 }
 
 moe_status_t check_dense(const moe_dense_config_t* c) {

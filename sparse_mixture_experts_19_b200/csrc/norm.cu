@@ -8,29 +8,38 @@
 //   dw = sum over rows of dy xh,  db = sum over rows of dy,
 // and optionally the residual stream's own gradient is added to dx.
 //
-// Both directions are bound by HBM: 2 flops or so per byte.  A row is read
-// once into registers (H <= 16384: up to four groups of 8 elements per
-// thread), so the two reductions of the forward (mean, then the squared
-// deviations from it: no cancellation) and the two sums of the backward need
-// no second read.  Every sum and statistic is float32; y and dx are rounded
-// once, to the layer type.
+// Both directions are bound by HBM (a few flops per byte), so the kernels are
+// built around bytes in flight: one CTA per SM, whose 16 warps form groups of
+// W warps, one row per group at a time.  Each group has a ring of S row slots
+// in shared memory that one thread fills with bulk copies (rows are
+// contiguous), up to 200 KB per SM on their way whatever the registers hold.
+// A row is read from HBM once; its statistics (forward: the mean, then the
+// squared deviations from it, so no cancellation; backward: the two sums) are
+// warp sums joined through shared memory with one barrier of the group each,
+// and that barrier is also what frees the previous row's slot.  Every sum and
+// statistic is float32; y and dx are rounded once, to the layer type.
 //
-// The weight gradients are sums over all rows.  Each CTA walks rows
-// blockIdx, blockIdx + grid, ... and keeps its own column sums in registers
-// (its threads own fixed columns), writes one partial row per CTA at the end,
-// and a second small kernel adds the partial rows in a fixed order: no
-// atomics, the same bits on every run.
+// The weight gradients are sums over all rows.  A thread owns fixed columns
+// and keeps their sums in registers over all its group's rows; a CTA adds its
+// groups in order and writes one partial row, and a second small kernel adds
+// the partial rows in a fixed order: no atomics, the same bits on every run.
 #include <algorithm>
 
 #include "common.cuh"
 #include "dense.cuh"
+#include "sm100.cuh"
 #include "tma_host.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarpRowMax = 1024;  // rows up to this long: one warp per row
-constexpr int kWarpsPerBlock = 8;  // of the warp-per-row kernels
+using namespace sm100;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRingBytes = 200 * 1024;
+constexpr int kMaxSlots = 8;
+constexpr int kMaxVpt = 4;  // groups of 8 elements per thread (2 where that is enough)
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
@@ -65,168 +74,337 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum of v over the threads of one row: the warp, or the whole block (every
-// thread gets the same bits).  `red` is one of two 32-float buffers used in
-// turn, so one barrier per sum is enough.
-template <bool kWarp>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-    v = warp_sum(v);
-    if (kWarp) return v;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    return warp_sum(lane < (int)(blockDim.x / 32) ? red[lane] : 0.f);
+// 8 consecutive elements of a row as they lie in memory.
+template <typename X>
+struct Raw8 {
+    uint4 q[sizeof(X) / 2];
+    __device__ __forceinline__ void load(const X* p) {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(X) / 2); ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (sizeof(X) == 4) {
+            const uint32_t u[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+        } else {
+            const uint32_t u[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(u[i] << 16);
+                v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+
+// A thread's columns of a float32 vector, or `other` where there is none.
+template <int kVpt>
+__device__ __forceinline__ void load_cols(float (&v)[kVpt][8], const float* p, int t, int threads, int H, float other) {
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i) {
+        const int c = (i * threads + t) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = other;
+        if (p && c < H) load8(p + c, v[i]);
+    }
 }
 
-template <typename X, int VPT, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerBlock : 512) norm_fwd_kernel(const NormArgs a) {
-    __shared__ float red[2][32];
-    const int g = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x % 32 : threadIdx.x;
-    const int64_t row = kWarp ? (int64_t)blockIdx.x * kWarpsPerBlock + threadIdx.x / 32 : blockIdx.x;
-    if (kWarp && row >= a.T) return;
-    const X* x = static_cast<const X*>(a.x) + row * a.H;
-    float v[VPT][8];
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (i * g + t) * 8;
-        if (c < a.H) {
-            load8(x + c, v[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s += v[i][j];
+// Geometry of a launch: W warps per row, S slots per group.
+struct Geo {
+    int W, S;
+    int slot_bytes;  // one row of every tensor that comes through the ring
+};
+
+// One group of W warps and its ring.
+struct Group {
+    int W, id, groups, t, threads;  // warps, index, groups per CTA, thread within, its threads
+    float (*red)[2][kWarps];        // [2][2][warps]
+    __device__ Group(int W_, float (*red_)[2][kWarps]) {
+        W = W_;
+        groups = kWarps / W;
+        id = threadIdx.x / (32 * W);
+        threads = 32 * W;
+        t = threadIdx.x - id * threads;
+        red = red_;
+    }
+    __device__ void sync() const {
+        if (W == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(threads) : "memory");
+    }
+    // Two warps' sums joined over the group: post, a sync, collect.
+    __device__ void post(float a, float b, int par) const {
+        const int warp = threadIdx.x / 32;
+        if (W > 1 && threadIdx.x % 32 == 0) {
+            red[par][0][warp] = a;
+            red[par][1][warp] = b;
         }
     }
+    __device__ void collect(float& a, float& b, int par) const {
+        const int lane = threadIdx.x % 32;
+        if (W > 1) {
+            a = warp_sum(lane < W ? red[par][0][id * W + lane] : 0.f);
+            b = warp_sum(lane < W ? red[par][1][id * W + lane] : 0.f);
+        }
+    }
+    // a and b summed over the group's threads (the same bits in each); par
+    // alternates from call to call, so that one barrier is enough.
+    __device__ void sum2(float& a, float& b, int par) const {
+        a = warp_sum(a);
+        b = warp_sum(b);
+        post(a, b, par);
+        sync();
+        collect(a, b, par);
+    }
+    __device__ float sum1(float a, int par) const {
+        a = warp_sum(a);
+        if (W > 1) {
+            const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+            if (lane == 0) red[par][0][warp] = a;
+            sync();
+            a = warp_sum(lane < W ? red[par][0][id * W + lane] : 0.f);
+        } else {
+            __syncwarp();
+        }
+        return a;
+    }
+};
+
+// Waits (bounded) for a slot's copies.  They are this CTA's own, so the wait
+// ends; should it not, the row's results become NaN rather than stale values.
+__device__ __forceinline__ float slot_wait(uint64_t* bar, uint32_t parity) {
+    return mbar_wait(bar, parity) ? 0.f : __int_as_float(0x7fffffff);
+}
+
+template <typename X, int kVpt>
+__global__ void __launch_bounds__(kThreads, 1) norm_fwd_kernel(const NormArgs a, const Geo geo) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float red[2][2][kWarps];
+    __shared__ uint64_t full[kWarps * kMaxSlots];
+    const Group g(geo.W, red);
+    uint8_t* ring = smem + (size_t)g.id * geo.S * geo.slot_bytes;
+    uint64_t* bar = full + g.id * geo.S;
+    const int64_t first = (int64_t)g.id * gridDim.x + blockIdx.x, step = (int64_t)g.groups * gridDim.x;
+    const X* x = static_cast<const X*>(a.x);
+    auto issue = [&](int64_t row, int s) {
+        mbar_arrive_expect_tx(&bar[s], geo.slot_bytes);
+        bulk_load(ring + s * geo.slot_bytes, x + row * a.H, geo.slot_bytes, &bar[s]);
+    };
+    if (g.t == 0) {
+        for (int s = 0; s < geo.S; ++s) mbar_init(&bar[s], 1);
+        fence_mbar_init();
+        for (int s = 0; s < geo.S; ++s)
+            if (first + s * step < a.T) issue(first + s * step, s);
+    }
+    g.sync();
+    // the thread's columns of w and b stay in registers over all its rows
+    float w[kVpt][8], b[kVpt][8];
+    load_cols(w, a.w, g.t, g.threads, a.H, 1.f);
+    load_cols(b, a.b, g.t, g.threads, a.H, 0.f);
     const float inv = 1.f / (float)a.H;
-    const float mu = a.layer ? row_sum<kWarp>(s, red[0]) * inv : 0.f;
-    s = 0.f;
+    int s = 0, par = 0;
+    uint32_t ph = 0;
+    for (int64_t row = first; row < a.T; row += step) {
+        const float bad = slot_wait(&bar[s], ph);
+        const X* src = reinterpret_cast<const X*>(ring + s * geo.slot_bytes);
+        Raw8<X> raw[kVpt];
+        float sum[2] = {bad, 0.f};
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        if ((i * g + t) * 8 < a.H) {
+        for (int i = 0; i < kVpt; ++i) {
+            const int c = (i * g.threads + g.t) * 8;
+            if (c < a.H) {
+                raw[i].load(src + c);
+                float v[8];
+                raw[i].get(v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i][j] -= mu;
-                s = fmaf(v[i][j], v[i][j], s);
+                for (int j = 0; j < 8; ++j) sum[j & 1] += v[j];
             }
         }
-    const float r = rsqrtf(row_sum<kWarp>(s, red[1]) * inv + a.eps);
-    if (t == 0) {
-        if (a.mean_out && a.layer) a.mean_out[row] = mu;
-        if (a.rstd_out) a.rstd_out[row] = r;
-    }
-    X* y = static_cast<X*>(a.y) + row * a.H;
+        float mu = bad;
+        if (a.layer) {
+            mu = g.sum1(sum[0] + sum[1], par) * inv;
+            par ^= 1;
+        }
+        sum[0] = sum[1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (i * g + t) * 8;
-        if (c < a.H) {
-            float w[8], b[8];
-            if (a.w) load8(a.w + c, w);
-            if (a.b) load8(a.b + c, b);
+        for (int i = 0; i < kVpt; ++i)
+            if ((i * g.threads + g.t) * 8 < a.H) {
+                float v[8];
+                raw[i].get(v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float xh = v[i][j] * r;
-                v[i][j] = a.w ? (a.b ? fmaf(xh, w[j], b[j]) : xh * w[j]) : (a.b ? xh + b[j] : xh);
+                for (int j = 0; j < 8; ++j) {
+                    const float d = v[j] - mu;
+                    sum[j & 1] = fmaf(d, d, sum[j & 1]);
+                }
             }
-            store8(y + c, v[i]);
+        const float r = rsqrtf(g.sum1(sum[0] + sum[1], par) * inv + a.eps);
+        par ^= 1;
+        // the sum's barrier: every warp of the group has this row in registers
+        if (g.t == 0) {
+            if (row + geo.S * step < a.T) issue(row + geo.S * step, s);
+            if (a.mean_out && a.layer) a.mean_out[row] = mu;
+            if (a.rstd_out) a.rstd_out[row] = r;
+        }
+        X* y = static_cast<X*>(a.y) + row * a.H;
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            const int c = (i * g.threads + g.t) * 8;
+            if (c < a.H) {
+                float v[8];
+                raw[i].get(v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = fmaf((v[j] - mu) * r, w[i][j], b[i][j]);
+                store8(y + c, v);
+            }
+        }
+        if (++s == geo.S) {
+            s = 0;
+            ph ^= 1;
         }
     }
 }
 
 // One partial row of dw (and of db) per CTA: part[blockIdx][0 dw, 1 db][H].
-template <typename X, typename G, int VPT, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerBlock : 512) norm_bwd_kernel(const NormArgs a) {
-    __shared__ float red[2][2][32];
-    __shared__ float cols[kWarp ? kWarpsPerBlock * kWarpRowMax : 1];
-    const int g = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x % 32 : threadIdx.x;
-    const int warp = threadIdx.x / 32;
-    const int64_t first = kWarp ? (int64_t)blockIdx.x * kWarpsPerBlock + warp : blockIdx.x;
-    const int64_t step = kWarp ? (int64_t)gridDim.x * kWarpsPerBlock : gridDim.x;
+template <typename X, typename G, int kVpt, bool kDb>
+__global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormArgs a, const Geo geo) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float red[2][2][kWarps];
+    __shared__ uint64_t full[kWarps * kMaxSlots];
+    const Group g(geo.W, red);
+    uint8_t* ring = smem + (size_t)g.id * geo.S * geo.slot_bytes;
+    uint64_t* bar = full + g.id * geo.S;
+    const int64_t first = (int64_t)g.id * gridDim.x + blockIdx.x, step = (int64_t)g.groups * gridDim.x;
+    const uint32_t xb = a.H * sizeof(X), gb = a.H * sizeof(G);
+    auto issue = [&](int64_t row, int s) {
+        uint8_t* dst = ring + s * geo.slot_bytes;
+        mbar_arrive_expect_tx(&bar[s], geo.slot_bytes);
+        bulk_load(dst, static_cast<const X*>(a.x) + row * a.H, xb, &bar[s]);
+        bulk_load(dst + xb, static_cast<const G*>(a.dy) + row * a.H, gb, &bar[s]);
+        if (a.d_res) bulk_load(dst + xb + gb, static_cast<const X*>(a.d_res) + row * a.H, xb, &bar[s]);
+    };
+    if (g.t == 0) {
+        for (int s = 0; s < geo.S; ++s) mbar_init(&bar[s], 1);
+        fence_mbar_init();
+        for (int s = 0; s < geo.S; ++s)
+            if (first + s * step < a.T) issue(first + s * step, s);
+    }
+    g.sync();
     const float inv = 1.f / (float)a.H;
-    float dw[VPT][8] = {}, db[VPT][8] = {};
-    int par = 0;
-    for (int64_t row = first; row < a.T; row += step, par ^= 1) {
-        const X* x = static_cast<const X*>(a.x) + row * a.H;
-        const G* dy = static_cast<const G*>(a.dy) + row * a.H;
-        const float r = a.rstd[row], mu = a.layer ? a.mean[row] : 0.f;
-        float xh[VPT][8], d[VPT][8];
-        float s1 = 0.f, s2 = 0.f;
+    float w[kVpt][8], dw[kVpt][8] = {}, db[kVpt][8] = {};
+    load_cols(w, a.w, g.t, g.threads, a.H, 1.f);
+    // Row k's two sums, then row k - 1's dx, between two barriers: the second
+    // half of the previous row covers the barrier and the warp sums of this one.
+    struct Row {
+        int s;
+        float mu, r, s1, s2;
+    };
+    auto sums = [&](int64_t row, int s, uint32_t ph, float r, float mu) {
+        Row o{s, mu + slot_wait(&bar[s], ph), r, 0.f, 0.f};
+        const X* x = reinterpret_cast<const X*>(ring + s * geo.slot_bytes);
+        const G* dy = reinterpret_cast<const G*>(ring + s * geo.slot_bytes + xb);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (i * g + t) * 8;
+        for (int i = 0; i < kVpt; ++i) {
+            const int c = (i * g.threads + g.t) * 8;
             if (c < a.H) {
-                load8(x + c, xh[i]);
-                load8(dy + c, d[i]);
-                float w[8];
-                if (a.w) load8(a.w + c, w);
+                float xh[8], d[8];
+                load8(x + c, xh);
+                load8(dy + c, d);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    xh[i][j] = (xh[i][j] - mu) * r;
-                    dw[i][j] = fmaf(d[i][j], xh[i][j], dw[i][j]);
-                    db[i][j] += d[i][j];
-                    if (a.w) d[i][j] *= w[j];
-                    s1 += d[i][j];
-                    s2 = fmaf(d[i][j], xh[i][j], s2);
+                    xh[j] = (xh[j] - o.mu) * r;
+                    dw[i][j] = fmaf(d[j], xh[j], dw[i][j]);
+                    if (kDb) db[i][j] += d[j];
+                    d[j] *= w[i][j];
+                    o.s1 += d[j];
+                    o.s2 = fmaf(d[j], xh[j], o.s2);
                 }
             }
         }
-        s2 = warp_sum(s2);
-        if (a.layer) s1 = warp_sum(s1);
-        if (!kWarp) {
-            const int lane = t % 32;
-            if (lane == 0) {
-                red[par][0][warp] = s1;
-                red[par][1][warp] = s2;
-            }
-            __syncthreads();
-            const bool in = lane < (int)(blockDim.x / 32);
-            s2 = warp_sum(in ? red[par][1][lane] : 0.f);
-            if (a.layer) s1 = warp_sum(in ? red[par][0][lane] : 0.f);
-        }
-        const float m1 = a.layer ? s1 * inv : 0.f, m2 = s2 * inv;
-        const X* res = a.d_res ? static_cast<const X*>(a.d_res) + row * a.H : nullptr;
+        return o;
+    };
+    auto finish = [&](int64_t row, const Row& o) {
+        const uint8_t* slot = ring + o.s * geo.slot_bytes;
+        const X* x = reinterpret_cast<const X*>(slot);
+        const G* dy = reinterpret_cast<const G*>(slot + xb);
+        const X* res = reinterpret_cast<const X*>(slot + xb + gb);
+        const float m1 = a.layer ? o.s1 * inv : 0.f, m2 = o.s2 * inv;
         X* dx = static_cast<X*>(a.dx) + row * a.H;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (i * g + t) * 8;
+        for (int i = 0; i < kVpt; ++i) {
+            const int c = (i * g.threads + g.t) * 8;
             if (c < a.H) {
-                float o[8];
-                if (res) load8(res + c, o);
+                float xh[8], d[8], v[8] = {};
+                load8(x + c, xh);
+                load8(dy + c, d);
+                if (a.d_res) load8(res + c, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float v = r * (d[i][j] - m1 - xh[i][j] * m2);
-                    o[j] = res ? v + o[j] : v;
+                    xh[j] = (xh[j] - o.mu) * o.r;
+                    v[j] += o.r * (fmaf(d[j], w[i][j], -m1) - xh[j] * m2);
                 }
-                store8(dx + c, o);
+                store8(dx + c, v);
             }
         }
+    };
+    int s = 0, par = 0;
+    uint32_t ph = 0;
+    if (geo.S == 1) {
+        for (int64_t row = first; row < a.T; row += step, ph ^= 1, par ^= 1) {
+            Row o = sums(row, 0, ph, a.rstd[row], a.layer ? a.mean[row] : 0.f);
+            g.sum2(o.s2, o.s1, par);
+            finish(row, o);
+            g.sync();
+            if (g.t == 0 && row + step < a.T) issue(row + step, 0);
+        }
+    } else if (first < a.T) {
+        Row last;
+        float r = a.rstd[first], mu = a.layer ? a.mean[first] : 0.f;
+        int64_t row = first;
+        for (; row < a.T; row += step, par ^= 1) {
+            const float r0 = r, mu0 = mu;
+            if (row + step < a.T) {  // the next row's statistics, ahead of their use
+                r = a.rstd[row + step];
+                mu = a.layer ? a.mean[row + step] : 0.f;
+            }
+            Row o = sums(row, s, ph, r0, mu0);
+            o.s1 = warp_sum(o.s1);
+            o.s2 = warp_sum(o.s2);
+            g.post(o.s2, o.s1, par);
+            if (row != first) finish(row - step, last);
+            g.sync();
+            g.collect(o.s2, o.s1, par);
+            // every warp of the group is done with the previous row
+            if (g.t == 0 && row != first && row + (geo.S - 1) * step < a.T)
+                issue(row + (geo.S - 1) * step, last.s);
+            last = o;
+            if (++s == geo.S) {
+                s = 0;
+                ph ^= 1;
+            }
+        }
+        finish(row - step, last);
     }
     if (!a.part) return;
+    // the CTA's groups, in order, through shared memory (the rings are empty)
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.H;
-    if (!kWarp) {
+    float* cols = reinterpret_cast<float*>(smem);
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (i * g + t) * 8;
-            if (c < a.H) {
-                store8(part + c, dw[i]);
-                store8(part + a.H + c, db[i]);
-            }
+    for (int which = 0; which < (kDb ? 2 : 1); ++which) {
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            const int c = (i * g.threads + g.t) * 8;
+            if (c < a.H) store8(cols + (size_t)g.id * a.H + c, which ? db[i] : dw[i]);
         }
-    } else {
-        // the block's warps in warp order, dw then db
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int c = (i * 32 + t) * 8;
-                if (c < a.H) store8(cols + warp * kWarpRowMax + c, which ? db[i] : dw[i]);
-            }
-            __syncthreads();
-            for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
-                float s = 0.f;
-                for (int k = 0; k < kWarpsPerBlock; ++k) s += cols[k * kWarpRowMax + c];
-                part[which * a.H + c] = s;
-            }
-            __syncthreads();
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.H; c += kThreads) {
+            float v = 0.f;
+            for (int k = 0; k < g.groups; ++k) v += cols[(size_t)k * a.H + c];
+            part[which * a.H + c] = v;
         }
+        __syncthreads();
     }
 }
 
@@ -251,48 +429,45 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* __restr
     if (threadIdx.y == 0 && c < N) out[c] = s[0][threadIdx.x];
 }
 
-struct Shape {
-    bool warp;
-    int vpt, threads;
-};
-
-// Rows up to 1024 elements take a warp each; longer rows a block of at most
-// 512 threads, with as few groups of 8 elements per thread as that allows.
-Shape shape_of(int H) {
-    const int g = (H + 7) / 8;
-    Shape s;
-    s.warp = H <= kWarpRowMax;
-    if (s.warp) {
-        s.vpt = g <= 32 ? 1 : (g <= 64 ? 2 : 4);
-        s.threads = 32 * kWarpsPerBlock;
-    } else {
-        s.vpt = g <= 256 ? 1 : (g <= 1024 ? 2 : 4);
-        const int per = (g + s.vpt - 1) / s.vpt;
-        s.threads = (per + 31) / 32 * 32;
-    }
-    return s;
+// Warps per row: as few as hold the row in kMaxVpt groups of 8 elements per
+// thread (32 x 32 elements per warp), so that a CTA has several independent
+// rows in flight; more when the slots of a group would otherwise be fewer than
+// three (two rows ahead of the one being worked on).
+Geo geo_of(int H, int slot_bytes) {
+    Geo g;
+    g.slot_bytes = slot_bytes;
+    g.W = 1;
+    while (g.W * 32 * 8 * kMaxVpt < H) g.W *= 2;
+    auto slots = [&] { return std::min(kMaxSlots, kRingBytes / (kWarps / g.W) / slot_bytes); };
+    while (g.W < kWarps && slots() < 3) g.W *= 2;
+    g.S = std::max(1, slots());
+    return g;
 }
 
-template <typename F>
-cudaError_t by_shape(const Shape& s, F f) {
-    if (s.warp) {
-        if (s.vpt == 1) return f(std::integral_constant<int, 1>(), std::true_type());
-        if (s.vpt == 2) return f(std::integral_constant<int, 2>(), std::true_type());
-        return f(std::integral_constant<int, 4>(), std::true_type());
-    }
-    if (s.vpt == 1) return f(std::integral_constant<int, 1>(), std::false_type());
-    if (s.vpt == 2) return f(std::integral_constant<int, 2>(), std::false_type());
-    return f(std::integral_constant<int, 4>(), std::false_type());
+bool two_vectors(const Geo& g, int H) { return g.W * 32 * 8 * 2 >= H; }
+
+int blocks_of(int64_t T) { return (int)std::min<int64_t>(T, kNormSms); }
+
+// Ring, or the float32 column sums of the CTA's groups at the end.
+size_t smem_of(const Geo& g, int H) {
+    const size_t groups = kWarps / g.W;
+    return std::max(groups * g.S * g.slot_bytes, groups * H * sizeof(float));
+}
+
+template <typename Kernel>
+cudaError_t launch(Kernel k, const NormArgs& a, const Geo& g, const char* name, cudaStream_t st) {
+    const size_t smem = smem_of(g, a.H);
+    cudaError_t e = ensure_smem_attr(k, kRingBytes);
+    if (e != cudaSuccess) return e;
+    trace_before(name, st);
+    k<<<blocks_of(a.T), kThreads, smem, st>>>(a, g);
+    trace_after(st);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-int norm_bwd_blocks(int64_t T, int H) {
-    const Shape s = shape_of(H);
-    const int64_t rows = s.warp ? (T + kWarpsPerBlock - 1) / kWarpsPerBlock : T;
-    const int per_sm = s.warp ? 2 : std::max(1, 1024 / s.threads);
-    return (int)std::min<int64_t>(rows, (int64_t)kNormBwdSms * per_sm);
-}
+int norm_bwd_blocks(int64_t T) { return blocks_of(T); }
 
 cudaError_t launch_sum_partials(const float* part, int64_t stride, int P, int64_t second, int N, float* out0,
                                 float* out1, cudaStream_t st) {
@@ -303,38 +478,34 @@ cudaError_t launch_sum_partials(const float* part, int64_t stride, int P, int64_
     return cudaGetLastError();
 }
 
+template <typename X>
+cudaError_t launch_fwd(const NormArgs& a, cudaStream_t st) {
+    const Geo g = geo_of(a.H, a.H * (int)sizeof(X));
+    return two_vectors(g, a.H) ? launch(norm_fwd_kernel<X, 2>, a, g, "norm_fwd", st)
+                               : launch(norm_fwd_kernel<X, kMaxVpt>, a, g, "norm_fwd", st);
+}
+
+template <typename X, typename G, bool kDb>
+cudaError_t launch_bwd(const NormArgs& a, cudaStream_t st) {
+    const Geo g = geo_of(a.H, a.H * (int)(sizeof(X) * (a.d_res ? 2 : 1) + sizeof(G)));
+    return two_vectors(g, a.H) ? launch(norm_bwd_kernel<X, G, 2, kDb>, a, g, "norm_bwd", st)
+                               : launch(norm_bwd_kernel<X, G, kMaxVpt, kDb>, a, g, "norm_bwd", st);
+}
+
 cudaError_t launch_norm_fwd(const NormArgs& a, bool f32, cudaStream_t st) {
-    const Shape s = shape_of(a.H);
-    const int64_t blocks = s.warp ? (a.T + kWarpsPerBlock - 1) / kWarpsPerBlock : a.T;
-    trace_before("norm_fwd", st);
-    by_shape(s, [&](auto vpt, auto warp) {
-        if (f32)
-            norm_fwd_kernel<float, vpt.value, warp.value><<<(unsigned)blocks, s.threads, 0, st>>>(a);
-        else
-            norm_fwd_kernel<bf16, vpt.value, warp.value><<<(unsigned)blocks, s.threads, 0, st>>>(a);
-        return cudaSuccess;
-    });
-    trace_after(st);
-    return cudaGetLastError();
+    return f32 ? launch_fwd<float>(a, st) : launch_fwd<bf16>(a, st);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, bool f32, bool dy_f32, cudaStream_t st) {
-    const Shape s = shape_of(a.H);
-    const int blocks = norm_bwd_blocks(a.T, a.H);
-    trace_before("norm_bwd", st);
-    by_shape(s, [&](auto vpt, auto warp) {
-        if (f32)
-            norm_bwd_kernel<float, float, vpt.value, warp.value><<<blocks, s.threads, 0, st>>>(a);
-        else if (dy_f32)
-            norm_bwd_kernel<bf16, float, vpt.value, warp.value><<<blocks, s.threads, 0, st>>>(a);
-        else
-            norm_bwd_kernel<bf16, bf16, vpt.value, warp.value><<<blocks, s.threads, 0, st>>>(a);
-        return cudaSuccess;
-    });
-    trace_after(st);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (a.db_out)
+        e = f32 ? launch_bwd<float, float, true>(a, st)
+                : (dy_f32 ? launch_bwd<bf16, float, true>(a, st) : launch_bwd<bf16, bf16, true>(a, st));
+    else
+        e = f32 ? launch_bwd<float, float, false>(a, st)
+                : (dy_f32 ? launch_bwd<bf16, float, false>(a, st) : launch_bwd<bf16, bf16, false>(a, st));
     if (e != cudaSuccess || !a.part) return e;
-    return launch_sum_partials(a.part, 2 * (int64_t)a.H, blocks, a.H, a.H, a.dw_out, a.db_out, st);
+    return launch_sum_partials(a.part, 2 * (int64_t)a.H, norm_bwd_blocks(a.T), a.H, a.H, a.dw_out, a.db_out, st);
 }
 
 }  // namespace moe
