@@ -14,6 +14,8 @@
 
 #include "act.cuh"
 #include "dense.cuh"
+#include "sm100.cuh"
+#include "tma_host.cuh"
 
 namespace moe {
 namespace {
@@ -44,6 +46,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 template <int kAct, bool kGated, bool kStore>
 __global__ void __launch_bounds__(32 * kLanes) dense_dz_kernel(const DenseDzArgs a) {
     __shared__ float red[kLanes][kCols + 4];
+    sm100::chain_next();
+    sm100::chain_wait();
     const int c = blockIdx.x * kCols + threadIdx.x * 8;
     const int64_t r0 = (int64_t)blockIdx.y * a.rows_per_block;
     const int64_t r1 = min(r0 + a.rows_per_block, (int64_t)a.T);
@@ -102,9 +106,11 @@ __global__ void __launch_bounds__(32 * kLanes) dense_dz_kernel(const DenseDzArgs
 
 // out[i] = sum over s < S of part[s * n + i], s in order, 4 per thread.
 template <typename O>
-__global__ void __launch_bounds__(256) sum_splits_kernel(const float* __restrict__ part, int64_t n, int S, int nout,
+__global__ void __launch_bounds__(256) sum_splits_kernel(const float* part, int64_t n, int S, int nout,
                                                          O* out0, O* out1) {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    sm100::chain_next();
+    sm100::chain_wait();
     if (i >= n) return;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s = 0; s < S; ++s) {
@@ -138,16 +144,13 @@ cudaError_t launch_dense_dz(DenseDzArgs a, bool gated, int act, float* db0, floa
     if (!(db0 || db1)) a.part = nullptr;
     const dim3 grid((a.N + kCols - 1) / kCols, rb), block(32, kLanes);
     trace_before(gated ? "gated_dgu" : "linear_dz", st);
+    cudaError_t e = cudaSuccess;
     by_act(act, [&](auto k) {
-        if (gated)
-            dense_dz_kernel<k.value, true, true><<<grid, block, 0, st>>>(a);
-        else if (store)
-            dense_dz_kernel<k.value, false, true><<<grid, block, 0, st>>>(a);
-        else
-            dense_dz_kernel<MOE_ACT_NONE, false, false><<<grid, block, 0, st>>>(a);
+        auto* fn = gated ? dense_dz_kernel<k.value, true, true>
+                         : (store ? dense_dz_kernel<k.value, false, true> : dense_dz_kernel<MOE_ACT_NONE, false, false>);
+        e = launch_chained(fn, grid, block, 0, 0, st, a);
     });
     trace_after(st);
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.part) return e;
     const int per = gated ? 2 : 1;
     return launch_sum_partials(a.part, (int64_t)per * a.N, rb, a.N, a.N, db0, gated ? db1 : nullptr, st);
@@ -158,12 +161,11 @@ cudaError_t launch_sum_splits(const float* part, int64_t n, int S, void* out0, v
     const int nout = out1 ? 2 : 1;
     const dim3 grid((unsigned)((n / 4 + 255) / 256), nout);
     trace_before("sum_splits", st);
-    if (f32)
-        sum_splits_kernel<float><<<grid, 256, 0, st>>>(part, n, S, nout, (float*)out0, (float*)out1);
-    else
-        sum_splits_kernel<bf16><<<grid, 256, 0, st>>>(part, n, S, nout, (bf16*)out0, (bf16*)out1);
+    const cudaError_t e =
+        f32 ? launch_chained(sum_splits_kernel<float>, grid, 256, 0, 0, st, part, n, S, nout, (float*)out0, (float*)out1)
+            : launch_chained(sum_splits_kernel<bf16>, grid, 256, 0, 0, st, part, n, S, nout, (bf16*)out0, (bf16*)out1);
     trace_after(st);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace moe

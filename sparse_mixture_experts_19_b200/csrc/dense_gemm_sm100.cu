@@ -14,9 +14,11 @@
 // rows x kBN columns, each CTA of the pair stages its own 128 rows of A and
 // half of B, and the leader issues M = 256 MMAs that read both CTAs' shared
 // memory: per CTA and 64-deep reduction step 32 KB arrive for 2 x 128 x 256 x
-// 64 flops, which keeps operand traffic below the tensor pipe's time.  TMEM
-// holds two accumulators, so a tile's epilogue overlaps the next tile's main
-// loop.  Bound by the tensor pipe at large sizes, by the stores (weight
+// 64 flops, which keeps operand traffic below the tensor pipe's time.  A stage
+// of the ring holds two steps: each wait for a stage and each commit holds up
+// the issuing thread's MMAs by about 120 ns, and with one step per stage they
+// were a fifth of the time.  TMEM holds two accumulators, so a tile's epilogue
+// overlaps the next tile's main loop.  Bound by the tensor pipe at large sizes, by the stores (weight
 // gradients of few tokens) or the operands' HBM reads otherwise.
 //
 // Roles (10 warps): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
@@ -48,7 +50,7 @@ constexpr int kTmemCols = 2 * kAccCols;
 constexpr int kABytes = kBM * kBK * 2;
 constexpr int kBox = 64 * kBK * 2;      // a 64 x 64 box of an MN-major operand
 constexpr int kEpiBuf = 32 * 128;       // 32 rows x 128 bytes
-constexpr int kEpiBytes = kEpiWarps * 2 * kEpiBuf;
+constexpr int kEpiBytes = kEpiWarps * kEpiBuf;
 
 // What a tile's epilogue does.
 enum Mode { kLinear = 0, kGated = 1, kF32 = 2 };
@@ -58,8 +60,9 @@ struct Cfg {
     static constexpr int kBHalf = kMode == kGated ? 128 : kBN / 2;  // B rows each CTA stages
     static constexpr int kMmaN = 2 * kBHalf;
     static constexpr int kBBytes = kBHalf * kBK * 2;
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = kBHalf == 128 ? 5 : 6;
+    static constexpr int kStepBytes = kABytes + kBBytes;  // one 64-deep step
+    static constexpr int kStageBytes = 2 * kStepBytes;    // a stage holds two
+    static constexpr int kStages = kBHalf == 128 ? 3 : 4;
     static constexpr size_t kEpiOff = (size_t)kStages * kStageBytes;
     static constexpr size_t kBarOff = kEpiOff + kEpiBytes;
     static constexpr size_t kSmem = kBarOff + 512 + 1024;
@@ -106,6 +109,12 @@ __device__ __forceinline__ Tile decode(int64_t t, const Args& a) {
     return ti;
 }
 
+// Steps of the stage that starts at ks: two, or one at the end of a segment or
+// of the tile's share of the reduction.
+__device__ __forceinline__ int stage_steps(int ks, const Tile& ti, const Args& a) {
+    return ks + 1 < ti.k1 && ks + 1 != a.seg_steps ? 2 : 1;
+}
+
 __device__ __forceinline__ uint32_t buf_off(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -145,9 +154,9 @@ __device__ __forceinline__ void store_buf(const CUtensorMap* map, uint32_t buf, 
     }
 }
 
-template <int kLeft>
-__device__ __forceinline__ void buffers_free(int lane) {
-    if (lane == 0) bulk_wait_read<kLeft>();
+// The warp's last store has read the staging buffer.
+__device__ __forceinline__ void buffer_free(int lane) {
+    if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
 }
 
@@ -165,8 +174,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     uint64_t* tfull = empty + C::kStages;
     uint64_t* tempty = tfull + 2;  // used in the leader: 8 epilogue warps x 2 CTAs
     uint64_t* drain = tempty + 2;
-    uint64_t* rbar = drain + 1;  // residual: 2 buffers x 8 warps
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(rbar + 2 * kEpiWarps);
+    uint64_t* rbar = drain + 1;  // residual chunks, one barrier per epilogue warp
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(rbar + kEpiWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -182,9 +191,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
             mbar_init(&tempty[i], 2 * kEpiWarps);
         }
         mbar_init(drain, 1);
-        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&rbar[i], 1);
+        for (int i = 0; i < kEpiWarps; ++i) mbar_init(&rbar[i], 1);
         *abort_flag = 0;
         fence_mbar_init();
+        tma_prefetch_map(&mA0);
+        tma_prefetch_map(&mB0);
+        tma_prefetch_map(&mD0);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_holder, kTmemCols);
@@ -194,40 +206,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    chain_next();
+    chain_wait();
     const int64_t pair = blockIdx.x / 2, npairs = gridDim.x / 2;
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer (both CTAs)
         if (lane == 0) {
-            tma_prefetch_map(&mA0);
-            tma_prefetch_map(&mB0);
             uint32_t it = 0;
             for (int64_t t = pair; t < a.total && !*abort_flag; t += npairs) {
                 const Tile ti = decode<kBN>(t, a);
                 const int arow = ti.m0 + (int)rank * kBM;
                 const int brow = kMode == kGated ? ti.n0 : ti.n0 + (int)rank * C::kBHalf;
-                for (int ks = ti.k0; ks < ti.k1; ++ks, ++it) {
+                for (int ks = ti.k0, n; ks < ti.k1; ks += n, ++it) {
+                    n = stage_steps(ks, ti, a);
                     const int s = it % C::kStages;
                     if (!wait_or_abort(&empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag, a.flags)) break;
                     const bool seg1 = ks >= a.seg_steps;
-                    const int kc = (seg1 ? ks - a.seg_steps : ks) * kBK;
                     const CUtensorMap* pA = seg1 || ti.prob ? &mA1 : &mA0;
                     const CUtensorMap* pB = seg1 || (kMode == kGated && rank) ? &mB1 : &mB0;
-                    uint8_t* sa = smem + s * C::kStageBytes;
-                    uint8_t* sb = sa + kABytes;
-                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
-                    if (kAMN) {
-                        tma_load_3d_pair(sa, pA, &full[s], arow, kc, 0);
-                        tma_load_3d_pair(sa + kBox, pA, &full[s], arow + 64, kc, 0);
-                    } else {
-                        tma_load_3d_pair(sa, pA, &full[s], kc, arow, 0);
-                    }
-                    if (kBMN) {
+                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * n * C::kStepBytes);
+                    for (int j = 0; j < n; ++j) {
+                        const int kc = (ks + j - (seg1 ? a.seg_steps : 0)) * kBK;
+                        uint8_t* sa = smem + s * C::kStageBytes + j * C::kStepBytes;
+                        uint8_t* sb = sa + kABytes;
+                        if (kAMN) {
+                            tma_load_3d_pair(sa, pA, &full[s], arow, kc, 0);
+                            tma_load_3d_pair(sa + kBox, pA, &full[s], arow + 64, kc, 0);
+                        } else {
+                            tma_load_3d_pair(sa, pA, &full[s], kc, arow, 0);
+                        }
+                        if (kBMN) {
 #pragma unroll
-                        for (int j = 0; j < C::kBHalf / 64; ++j)
-                            tma_load_3d_pair(sb + j * kBox, pB, &full[s], brow + 64 * j, kc, 0);
-                    } else {
-                        tma_load_3d_pair(sb, pB, &full[s], kc, brow, 0);
+                            for (int i = 0; i < C::kBHalf / 64; ++i)
+                                tma_load_3d_pair(sb + i * kBox, pB, &full[s], brow + 64 * i, kc, 0);
+                        } else {
+                            tma_load_3d_pair(sb, pB, &full[s], kc, brow, 0);
+                        }
                     }
                 }
             }
@@ -238,9 +253,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader)
+        // One thread's instruction stream paces the tensor core, so it is kept
+        // short: descriptors by addition, the next step's barrier tested while
+        // this step's MMAs are being issued.
         if (lane == 0 && leader) {
             constexpr uint32_t kIdesc = idesc_bf16_major(2 * kBM, C::kMmaN, kAMN, kBMN);
-            uint32_t it = 0, tc = 0;
+            constexpr uint32_t kStepA = (kAMN ? 2048 : 32) >> 4, kStepB = (kBMN ? 2048 : 32) >> 4;
+            const uint32_t base = smem_u32(smem);
+            const uint64_t da0 = kAMN ? desc_mnmajor_sw128(base, kBox, 1024) : desc_kmajor_sw128(base);
+            const uint64_t db0 = kBMN ? desc_mnmajor_sw128(base + kABytes, kBox, 1024) : desc_kmajor_sw128(base + kABytes);
+            uint32_t s = 0, ph = 0, tc = 0;
+            bool ready = false;
             for (int64_t t = pair; t < a.total && !*abort_flag; t += npairs, ++tc) {
                 const Tile ti = decode<kBN>(t, a);
                 const uint32_t acc = tc & 1;
@@ -248,23 +271,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * kAccCols;
                 bool ok = true;
-                for (int ks = ti.k0; ks < ti.k1; ++ks, ++it) {
-                    const int s = it % C::kStages;
-                    if (!wait_or_abort(&full[s], (it / C::kStages) & 1, abort_flag, a.flags)) {
+                uint32_t sum = 0;
+                for (int ks = ti.k0, n; ks < ti.k1; ks += n) {
+                    n = stage_steps(ks, ti, a);
+                    if (!ready && !wait_or_abort(&full[s], ph, abort_flag, a.flags)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(smem + s * C::kStageBytes), b0 = a0 + kABytes;
-#pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk) {
-                        const uint64_t da = kAMN ? desc_mnmajor_sw128(a0 + kk * 2048, kBox, 1024)
-                                                 : desc_kmajor_sw128(a0 + kk * 32);
-                        const uint64_t db = kBMN ? desc_mnmajor_sw128(b0 + kk * 2048, kBox, 1024)
-                                                 : desc_kmajor_sw128(b0 + kk * 32);
-                        mma_bf16_pair(d, da, db, kIdesc, ks > ti.k0 || kk > 0);
+                    const uint32_t cur = s;
+                    if (++s == C::kStages) {
+                        s = 0;
+                        ph ^= 1;
                     }
-                    mma_commit_pair(&empty[s], 0x3);  // frees the stage in both CTAs
+                    ready = mbar_test(&full[s], ph);
+                    uint64_t da = da0 + cur * (C::kStageBytes >> 4), db = db0 + cur * (C::kStageBytes >> 4);
+                    for (int j = 0; j < n; ++j, da += C::kStepBytes >> 4, db += C::kStepBytes >> 4)
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; ++kk) {
+                            mma_bf16_pair(d, da + kk * kStepA, db + kk * kStepB, kIdesc, sum);
+                            sum = 1;
+                        }
+                    mma_commit_pair(&empty[cur], 0x3);  // frees the stage in both CTAs
                 }
                 if (!ok) break;
                 mma_commit_pair(&tfull[acc], 0x3);
@@ -275,52 +303,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     } else {
         // ------------------------------------------------ epilogue (both CTAs)
         const int e = warp - 2, q = warp & 3, half = e >> 2;
-        const uint32_t buf0 = smem_u32(smem + C::kEpiOff) + (uint32_t)e * 2 * kEpiBuf;
+        uint8_t* buf_ptr = smem + C::kEpiOff + (size_t)e * kEpiBuf;
+        const uint32_t buf = smem_u32(buf_ptr);
         constexpr int kHalfCols = (kMode == kGated ? 128 : kBN) / 2;  // output columns of this warp
-        constexpr int kChunk = kMode == kF32 ? 32 : 64;               // columns of one staging buffer
+        constexpr int kChunk = kMode == kF32 ? 32 : 64;               // columns of the staging buffer
         constexpr int kChunks = kHalfCols / kChunk;
-        uint32_t tc = 0, rph = 0, nb = 0;  // rph bit j: phase of residual buffer j
+        uint32_t tc = 0, rph = 0;
         for (int64_t t = pair; t < a.total; t += npairs, ++tc) {
             const Tile ti = decode<kBN>(t, a);
             const uint32_t acc = tc & 1;
             const int row = ti.m0 + (int)rank * kBM + q * 32;
             const int col0 = ti.n0 + half * kHalfCols;
             const bool rows_in = row < a.M;
-            if (kMode == kLinear && a.has_res && rows_in) {
-                // the residual chunks into the staging buffers, ahead of the accumulator
-                buffers_free<0>(lane);
-                if (lane == 0)
-#pragma unroll
-                    for (int j = 0; j < kChunks; ++j)
-                        if (col0 + j * kChunk < a.N) {
-                            mbar_arrive_expect_tx(&rbar[2 * e + j], kEpiBuf);
-                            tma_load_3d(smem + C::kEpiOff + (e * 2 + j) * kEpiBuf, &mR, &rbar[2 * e + j],
-                                        col0 + j * kChunk, row, 0);
-                        }
-            }
-            const bool ok = wait_sleep_or_abort(&tfull[acc], (tc >> 1) & 1, abort_flag, a.flags);
-            if (!ok) {
-                if (kMode == kLinear && a.has_res && rows_in)
-                    for (int j = 0; j < kChunks; ++j)
-                        if (col0 + j * kChunk < a.N) drain_wait(&rbar[2 * e + j], (rph >> j) & 1);
+            // chunk j's residual into the staging buffer
+            auto fetch_res = [&](int j) {
+                buffer_free(lane);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&rbar[e], kEpiBuf);
+                    tma_load_3d(buf_ptr, &mR, &rbar[e], col0 + j * kChunk, row, 0);
+                }
+            };
+            const bool res = kMode == kLinear && a.has_res;
+            const bool ahead = res && rows_in && col0 < a.N;
+            if (ahead) fetch_res(0);  // ahead of the accumulator
+            if (!wait_sleep_or_abort(&tfull[acc], (tc >> 1) & 1, abort_flag, a.flags)) {
+                if (ahead) drain_wait(&rbar[e], rph);
                 break;
             }
             tc_fence_after();
             const uint32_t tq = tmem_base + acc * kAccCols + ((uint32_t)(q * 32) << 16) + half * kHalfCols;
+            auto accumulator_free = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(&tempty[acc], 0);
+            };
             if (kMode == kF32) {
 #pragma unroll 1
                 for (int j = 0; j < kChunks; ++j) {
                     float v[32];
                     tmem_ld32(tq + j * 32, v);
-                    if (j == kChunks - 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(&tempty[acc], 0);
-                    }
+                    if (j == kChunks - 1) accumulator_free();
                     const int col = col0 + j * 32;
                     if (!rows_in || col >= a.N) continue;
-                    const uint32_t buf = buf0 + (nb++ & 1) * kEpiBuf;
-                    buffers_free<1>(lane);
+                    buffer_free(lane);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         st_shared_u4(buf + buf_off(lane, i), __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
@@ -330,33 +355,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                               parts ? ti.split * a.problems + ti.prob : 0);
                 }
             } else if (kMode == kGated) {
+                const bool live = rows_in && col0 < a.N;
+                if (live) {
+                    // the kept projections first, one at a time through the buffer
+#pragma unroll 1
+                    for (int p = 0; p < 2; ++p) {
+                        if (!(p ? a.has_z1 : a.has_z0)) continue;
+                        buffer_free(lane);
+#pragma unroll
+                        for (int sub = 0; sub < 2; ++sub) {
+                            float v[32];
+                            tmem_ld32(tq + 128 * p + 32 * sub, v);
+                            add_bias(v, p ? a.bias1 : a.bias0, col0 + 32 * sub, a.N);
+                            uint32_t o[16];
+                            pack32(v, o);
+                            stage16(buf, lane, sub, o);
+                        }
+                        store_buf(p ? &mD2 : &mD1, buf, lane, col0, row, 0);
+                    }
+                }
                 uint32_t h[32];
-                const int col = col0;
-                const bool live = rows_in && col < a.N;
-                const bool keep = a.has_z0 || a.has_z1;
-                if (live && keep) buffers_free<0>(lane);
 #pragma unroll
                 for (int sub = 0; sub < 2; ++sub) {
                     float g[32], u[32];
                     tmem_ld32(tq + 32 * sub, g);
                     tmem_ld32(tq + 128 + 32 * sub, u);
-                    if (sub == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(&tempty[acc], 0);
-                    }
+                    if (sub == 1) accumulator_free();
                     if (!live) continue;
-                    add_bias(g, a.bias0, col + 32 * sub, a.N);
-                    add_bias(u, a.bias1, col + 32 * sub, a.N);
-                    uint32_t o[16];
-                    if (a.has_z0) {
-                        pack32(g, o);
-                        stage16(buf0, lane, sub, o);
-                    }
-                    if (a.has_z1) {
-                        pack32(u, o);
-                        stage16(buf0 + kEpiBuf, lane, sub, o);
-                    }
+                    add_bias(g, a.bias0, col0 + 32 * sub, a.N);
+                    add_bias(u, a.bias1, col0 + 32 * sub, a.N);
                     by_act(a.act, [&](auto k) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) g[i] = act_value<k.value>(g[i]) * u[i];
@@ -364,35 +391,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                     pack32(g, h + 16 * sub);
                 }
                 if (live) {
-                    if (a.has_z0) store_buf(&mD1, buf0, lane, col, row, 0);
-                    if (a.has_z1) store_buf(&mD2, buf0 + kEpiBuf, lane, col, row, 0);
-                    const uint32_t buf = buf0 + (keep ? 0 : nb & 1) * kEpiBuf;
-                    if (a.has_z0 && a.has_z1)
-                        buffers_free<1>(lane);  // g's store has read buffer 0
-                    else if (keep)
-                        buffers_free<0>(lane);
-                    else
-                        buffers_free<1>(lane);
-                    ++nb;
+                    buffer_free(lane);
                     stage16(buf, lane, 0, h);
                     stage16(buf, lane, 1, h + 16);
-                    store_buf(&mD0, buf, lane, col, row, 0);
+                    store_buf(&mD0, buf, lane, col0, row, 0);
                 }
             } else {
 #pragma unroll 1
                 for (int j = 0; j < kChunks; ++j) {
                     const int col = col0 + j * kChunk;
                     const bool live = rows_in && col < a.N;
-                    const bool z = a.has_z0, res = a.has_res;
-                    // with a residual the chunk's buffer is the one it arrived in
-                    const uint32_t buf = buf0 + (res ? j : nb & 1) * kEpiBuf;
                     if (live) {
-                        if (res) {
-                            const bool got = wait_or_abort(&rbar[2 * e + j], (rph >> j) & 1, abort_flag, a.flags);
-                            if (!got) drain_wait(&rbar[2 * e + j], (rph >> j) & 1);
-                            rph ^= 1u << j;
+                        if (!res) {
+                            buffer_free(lane);
                         } else {
-                            buffers_free<1>(lane);
+                            if (j > 0) fetch_res(j);
+                            if (!wait_or_abort(&rbar[e], rph, abort_flag, a.flags)) drain_wait(&rbar[e], rph);
+                            rph ^= 1;
                         }
                     }
                     uint32_t y[32];
@@ -400,11 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                     for (int sub = 0; sub < 2; ++sub) {
                         float v[32];
                         tmem_ld32(tq + j * kChunk + 32 * sub, v);
-                        if (j == kChunks - 1 && sub == 1) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster(&tempty[acc], 0);
-                        }
+                        if (j == kChunks - 1 && sub == 1) accumulator_free();
                         if (!live) continue;
                         add_bias(v, a.bias0, col + 32 * sub, a.N);
                         uint32_t r[16];
@@ -414,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                                 const uint4 w = ld_shared_u4(buf + buf_off(lane, 4 * sub + i));
                                 r[4 * i] = w.x, r[4 * i + 1] = w.y, r[4 * i + 2] = w.z, r[4 * i + 3] = w.w;
                             }
-                        if (z) {
+                        if (a.has_z0) {  // in the place of the residual just read
                             uint32_t o[16];
                             pack32(v, o);
                             stage16(buf, lane, sub, o);
@@ -432,15 +443,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                         pack32(v, y + 16 * sub);
                     }
                     if (live) {
-                        if (z) {
+                        if (a.has_z0) {
                             store_buf(&mD1, buf, lane, col, row, 0);
-                            buffers_free<0>(lane);
+                            buffer_free(lane);
                         }
                         stage16(buf, lane, 0, y);
                         stage16(buf, lane, 1, y + 16);
-                        const bool second = ti.prob != 0;
-                        store_buf(second ? &mD1 : &mD0, buf, lane, col, row, 0);
-                        ++nb;
+                        store_buf(ti.prob ? &mD1 : &mD0, buf, lane, col, row, 0);
                     }
                 }
             }
@@ -473,9 +482,9 @@ cudaError_t launch(const Maps& m, Args a, const char* name, cudaStream_t st) {
     const int pairs = device_sm_count() / 2;
     const int grid = 2 * (int)std::max<int64_t>(1, std::min<int64_t>(pairs, a.total));
     trace_before(name, st);
-    fn<<<grid, kThreads, C::kSmem, st>>>(m.A0, m.A1, m.B0, m.B1, m.D0, m.D1, m.D2, m.R, a);
+    e = launch_chained(fn, grid, kThreads, C::kSmem, 0, st, m.A0, m.A1, m.B0, m.B1, m.D0, m.D1, m.D2, m.R, a);
     trace_after(st);
-    return cudaGetLastError();
+    return e;
 }
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
@@ -486,12 +495,14 @@ int band_of(int64_t k) {
     return (int)std::min<int64_t>(std::max<int64_t>(g, 8), 1 << 20);
 }
 
-// Column tile: 256, or 128 when its finer grid leaves fewer idle pairs in the
-// last wave by more than the 6% that its larger operand traffic costs.
+// Column tile: 256, or 128 when its finer grid wins.  A 128-column tile takes
+// 0.82 of a 256-column tile's time (its 24 KB per reduction step against 32 KB
+// are bound by the loads; measured at T = 2048, 4096 -> 14336: 278 against 171
+// us), so it pays only where the last wave would leave most pairs idle.
 bool narrow_tiles(int64_t M, int64_t N, int64_t copies) {
-    const int64_t pairs = kDensePairs, mt = cdiv(M, 2 * kBM) * copies;
-    const double wide = (double)((mt * cdiv(N, 256) + pairs - 1) / pairs) * 2;
-    const double narrow = (double)((mt * cdiv(N, 128) + pairs - 1) / pairs) * 1.06;
+    const int64_t mt = cdiv(M, 2 * kBM) * copies;
+    const double wide = (double)cdiv(mt * cdiv(N, 256), kDensePairs);
+    const double narrow = (double)cdiv(mt * cdiv(N, 128), kDensePairs) * 0.82;
     return narrow < wide;
 }
 

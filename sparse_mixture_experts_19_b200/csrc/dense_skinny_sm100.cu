@@ -3,15 +3,18 @@
 // HBM is the bound.
 //
 // The weights take the tensor core's 128-row side and the tokens its column
-// side: D[128 output features][kTN tokens], so a call of one token wastes 15
+// side: D[128 output features][tn tokens], so a call of one token wastes 15
 // columns of a cheap MMA instead of 255 rows, and every SM spends its time on
 // weight bytes.  A CTA owns one tile and one share of the reduction: a cluster
 // of S <= 8 CTAs splits the reduction (enough clusters to cover the SMs when
-// the output has few feature tiles), each streams its share through a TMA ring
-// of up to 200 KB (weights 16 KB per 64-deep step, read once), and the S
-// partial tiles are added through distributed shared memory in rank order:
-// CTA r finishes the r-th share of the tokens.  The sum's order depends on the
-// sizes alone, so the bits do not change from run to run.
+// the output has few feature tiles), and each streams its share through a TMA
+// ring of up to 200 KB (weights 16 KB per 64-deep step, read once).  Then every
+// CTA pushes to CTA r, by bulk copies through distributed shared memory, its
+// partial sums of the r-th share of the tokens, and CTA r adds the S partials
+// in rank order and finishes them.  (Pulling them with loads from the peers
+// instead took 4 us of a 9 us call of 64 tokens: few loads in flight against
+// the latency of remote shared memory.)  The sum's order depends on the sizes
+// alone, so the bits do not change from run to run.
 //
 //   forward: A = W rows K-major; gated: two A tiles (gate, up) and two
 //            accumulators per step
@@ -39,8 +42,9 @@ constexpr int kThreads = 192;
 constexpr int kABytes = 128 * kBK * 2;
 constexpr int kBox = 64 * kBK * 2;
 constexpr int kMaxStages = 12;
-constexpr int kRingBytes = 208 * 1024;
-constexpr size_t kSmem = kRingBytes + 512 + 1024;
+constexpr int kDataBytes = 208 * 1024;  // ring, and the received partial sums behind it
+constexpr size_t kSmem = kDataBytes + 512 + 1024;
+constexpr int kRowBytes = 128 * 4;  // one token's 128 features, float32
 
 struct Args {
     int T, N;        // tokens, output features
@@ -48,6 +52,8 @@ struct Args {
     int stages;
     int seg_steps, steps;
     int splits;      // CTAs per cluster
+    int slice;       // splits > 1: most tokens one CTA of the cluster finishes
+    int recv_off;    // splits > 1: received partials [split][accumulator][slice][128]
     int act;
     const float* bias0;
     const float* bias1;
@@ -59,9 +65,9 @@ struct Args {
     int32_t* flags;
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
     float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                  : "r"(addr)
                  : "memory");
@@ -82,10 +88,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
                                                                    const Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kDataBytes);
     uint64_t* empty = full + kMaxStages;
     uint64_t* done = empty + kMaxStages;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* recv = done + 1;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(recv + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -94,46 +101,64 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
     const int ks0 = (int)((int64_t)a.steps * rank / a.splits), ks1 = (int)((int64_t)a.steps * (rank + 1) / a.splits);
     const int b_bytes = a.tn * kBK * 2;
     const int stage_bytes = (kGated ? 2 : 1) * kABytes + b_bytes;
+    constexpr int kAcc = kGated ? 2 : 1;
+    const int tokens = min(a.tn, a.T - t0);
+    // tokens CTA r of the cluster finishes
+    auto share = [&](int r) { return tokens * r / a.splits; };
+    const int tk0 = share((int)rank), tk1 = share((int)rank + 1);
+    auto load_step = [&](int ks, int s) {
+        const bool seg1 = ks >= a.seg_steps;
+        const int kc = (seg1 ? ks - a.seg_steps : ks) * kBK;
+        uint8_t* sa = smem + s * stage_bytes;
+        uint8_t* sb = sa + (kGated ? 2 : 1) * kABytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        if (kAMN) {
+            const CUtensorMap* pA = seg1 ? &mA1 : &mA0;
+            tma_load_3d(sa, pA, &full[s], n0, kc, 0);
+            tma_load_3d(sa + kBox, pA, &full[s], n0 + 64, kc, 0);
+        } else {
+            tma_load_3d(sa, &mA0, &full[s], kc, n0, 0);
+            if (kGated) tma_load_3d(sa + kABytes, &mA1, &full[s], kc, n0, 0);
+        }
+        tma_load_3d(sb, seg1 ? &mB1 : &mB0, &full[s], kc, t0, 0);
+    };
+    const int first = min(a.stages, ks1 - ks0);  // steps that need no free slot
     if (threadIdx.x == 0) {
+        tma_prefetch_map(&mA0);
+        tma_prefetch_map(&mB0);
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
+        mbar_init(recv, 1);
         *abort_flag = 0;
         fence_mbar_init();
+        if (a.splits > 1 && tk1 > tk0) mbar_arrive_expect_tx(recv, (uint32_t)(a.splits * kAcc * (tk1 - tk0) * kRowBytes));
+        chain_wait();
+        for (int s = 0; s < first; ++s) load_step(ks0 + s, s);
     }
     if (warp == 1) {
         tmem_alloc(tmem_holder, a.tmem_cols);
         tmem_relinquish();
     }
+    chain_next();
+    chain_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    if (a.splits > 1) cluster_arrive();  // this CTA's barriers exist (waited for before the first push)
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 1;
-            int it = 0;
-            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+            int s = first == a.stages ? 0 : first;
+            uint32_t ph = 0;
+            int it = first;
+            for (int ks = ks0 + first; ks < ks1; ++ks, ++it) {
                 if (!wait_or_abort(&empty[s], ph, abort_flag, a.flags)) break;
-                const bool seg1 = ks >= a.seg_steps;
-                const int kc = (seg1 ? ks - a.seg_steps : ks) * kBK;
-                uint8_t* sa = smem + s * stage_bytes;
-                uint8_t* sb = sa + (kGated ? 2 : 1) * kABytes;
-                mbar_arrive_expect_tx(&full[s], stage_bytes);
-                if (kAMN) {
-                    const CUtensorMap* pA = seg1 ? &mA1 : &mA0;
-                    tma_load_3d(sa, pA, &full[s], n0, kc, 0);
-                    tma_load_3d(sa + kBox, pA, &full[s], n0 + 64, kc, 0);
-                } else {
-                    tma_load_3d(sa, &mA0, &full[s], kc, n0, 0);
-                    if (kGated) tma_load_3d(sa + kABytes, &mA1, &full[s], kc, n0, 0);
-                }
-                tma_load_3d(sb, seg1 ? &mB1 : &mB0, &full[s], kc, t0, 0);
+                load_step(ks, s);
                 if (++s == a.stages) {
                     s = 0;
                     ph ^= 1;
@@ -174,94 +199,145 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
     } else {
         // ------------------------------------------------ TMEM -> partial tile in shared memory
         // (the ring is free: the accumulator is complete, so every step's
-        // operands have been read).  part[acc][token][128 features]
+        // operands have been read).  part[accumulator][token][128 features]
         const int q = warp & 3;
-        const bool ok = wait_sleep_or_abort(done, 0, abort_flag, a.flags);
+        wait_sleep_or_abort(done, 0, abort_flag, a.flags);
         tc_fence_after();
         float* part = reinterpret_cast<float*>(smem);
-        const int cols = (kGated ? 2 : 1) * a.tn;
-        if (ok)
-            for (int c = 0; c < cols; c += 16) {
-                float v[16];
-                tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + c, v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) part[(c + i) * 128 + q * 32 + lane] = ks1 > ks0 ? v[i] : 0.f;
+        for (int p = 0; p < kAcc; ++p)
+            for (int c = 0; c < tokens; c += 16) {
+                float v[16];
+                tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + p * a.tn + c, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) part[(p * a.tn + c + i) * 128 + q * 32 + lane] = v[i];
             }
         tc_fence_before();
+        if (a.splits > 1) fence_async_smem();
     }
     __syncwarp();  // the single-lane roles join their warps
-    if (a.splits > 1)
-        cluster_sync();
-    else
-        __syncthreads();
+    __syncthreads();
+    uint32_t src = smem_u32(smem);  // partial sums, and how they are laid out
+    int src_tok = 0, src_acc = a.tn * kRowBytes, src_rank = 0;
+    bool got = true;
+    if (a.splits > 1) {
+        cluster_wait();
+        if (warp == 0 && lane < a.splits) {
+            const int d0 = share(lane), d1 = share(lane + 1);
+            const uint32_t bar = mapa_shared(smem_u32(recv), lane);
+            const uint32_t dst = mapa_shared(src + a.recv_off, lane) + rank * kAcc * a.slice * kRowBytes;
+            if (d1 > d0)
+#pragma unroll
+                for (int p = 0; p < kAcc; ++p)
+                    bulk_push(dst + p * a.slice * kRowBytes, src + (p * a.tn + d0) * kRowBytes, (d1 - d0) * kRowBytes,
+                              bar);
+        }
+        __syncwarp();
+        if (tk1 > tk0) got = wait_sleep_or_abort(recv, 0, abort_flag, a.flags);
+        if (!got) drain_wait(recv, 0);
+        __syncwarp();
+        cluster_arrive();  // received: the senders' tiles are free (waited for before the exit)
+        src += a.recv_off;
+        src_tok = tk0;
+        src_acc = a.slice * kRowBytes;
+        src_rank = kAcc * a.slice * kRowBytes;
+    }
 
     // ---------------------------------------------------- finish: 4 features of a token per thread
-    const int tokens = min(a.tn, a.T - t0);
-    const int tk0 = tokens * (int)rank / a.splits, tk1 = tokens * ((int)rank + 1) / a.splits;
-    const uint32_t base = smem_u32(smem);
-    for (int i = tk0 * 32 + (int)threadIdx.x; i < tk1 * 32; i += kThreads) {
-        const int tok = i / 32, f = (i % 32) * 4, n = n0 + f;
-        if (n >= a.N) continue;  // N is a multiple of 8
-        float v[2][4];
+    // and item, kItems items at once so that their loads are in flight together
+    constexpr int kItems = kGated ? 2 : 4;
+    const int f = lane * 4, n = n0 + f;  // a warp spans the tile's 128 features
+    if (got && n < a.N) {                // N is a multiple of 8
+        float4 bias[kAcc];
 #pragma unroll
-        for (int p = 0; p < (kGated ? 2 : 1); ++p) {
-            const uint32_t off = base + (uint32_t)(((p * a.tn + tok) * 128 + f) * 4);
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < kAcc; ++p) {
+            const float* b = p ? a.bias1 : a.bias0;
+            bias[p] = b ? *reinterpret_cast<const float4*>(b + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int tok0 = tk0 + warp; tok0 < tk1; tok0 += kItems * (kThreads / 32)) {
+            uint2 res[kItems];
+            float4 s[kItems][kAcc];
+#pragma unroll
+            for (int u = 0; u < kItems; ++u) {
+                const int tok = tok0 + u * (kThreads / 32);
+                res[u] = make_uint2(0u, 0u);
+                if (a.res && tok < tk1) res[u] = *reinterpret_cast<const uint2*>(a.res + (int64_t)(t0 + tok) * a.N + n);
+#pragma unroll
+                for (int p = 0; p < kAcc; ++p) s[u][p] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
             for (int r = 0; r < a.splits; ++r) {
-                const float4 w = ld_cluster_f4(a.splits > 1 ? mapa_shared(off, r) : off);
-                s.x += w.x, s.y += w.y, s.z += w.z, s.w += w.w;
-            }
-            const float* bias = p ? a.bias1 : a.bias0;
-            if (bias) {
-                const float4 b = *reinterpret_cast<const float4*>(bias + n);
-                s.x += b.x, s.y += b.y, s.z += b.z, s.w += b.w;
-            }
-            v[p][0] = s.x, v[p][1] = s.y, v[p][2] = s.z, v[p][3] = s.w;
-        }
-        const int64_t o = (int64_t)(t0 + tok) * a.N + n;
-        if (a.z0) store4(a.z0 + o, v[0]);
-        if (kGated && a.z1) store4(a.z1 + o, v[1]);
-        by_act(a.act, [&](auto k) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[0][j] = act_value<k.value>(v[0][j]);
-        });
-        if (kGated)
+                for (int u = 0; u < kItems; ++u) {
+                    const int tok = min(tok0 + u * (kThreads / 32), tk1 - 1) - src_tok;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[0][j] *= v[1][j];
-        if (a.res) {
-            const uint2 w = *reinterpret_cast<const uint2*>(a.res + o);
-            v[0][0] += __uint_as_float(w.x << 16), v[0][1] += __uint_as_float(w.x & 0xffff0000u);
-            v[0][2] += __uint_as_float(w.y << 16), v[0][3] += __uint_as_float(w.y & 0xffff0000u);
+                    for (int p = 0; p < kAcc; ++p) {
+                        const float4 w = ld_shared_f4(src + r * src_rank + p * src_acc + tok * kRowBytes + f * 4);
+                        s[u][p].x += w.x, s[u][p].y += w.y, s[u][p].z += w.z, s[u][p].w += w.w;
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kItems; ++u) {
+                const int tok = tok0 + u * (kThreads / 32);
+                if (tok >= tk1) break;
+                float v[kAcc][4];
+#pragma unroll
+                for (int p = 0; p < kAcc; ++p) {
+                    v[p][0] = s[u][p].x + bias[p].x, v[p][1] = s[u][p].y + bias[p].y;
+                    v[p][2] = s[u][p].z + bias[p].z, v[p][3] = s[u][p].w + bias[p].w;
+                }
+                const int64_t o = (int64_t)(t0 + tok) * a.N + n;
+                if (a.z0) store4(a.z0 + o, v[0]);
+                if (kGated && a.z1) store4(a.z1 + o, v[kAcc - 1]);
+                by_act(a.act, [&](auto k) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[0][j] = act_value<k.value>(v[0][j]);
+                });
+                if (kGated)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[0][j] *= v[kAcc - 1][j];
+                v[0][0] += __uint_as_float(res[u].x << 16), v[0][1] += __uint_as_float(res[u].x & 0xffff0000u);
+                v[0][2] += __uint_as_float(res[u].y << 16), v[0][3] += __uint_as_float(res[u].y & 0xffff0000u);
+                store4(a.y + o, v[0]);
+            }
         }
-        store4(a.y + o, v[0]);
     }
-    if (a.splits > 1)
-        cluster_sync();  // the peers have read this CTA's partial tile
-    else
-        __syncthreads();
+    __syncwarp();
+    if (a.splits > 1) cluster_wait();  // every peer has received this CTA's partial sums
+    __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, a.tmem_cols);
 }
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Tokens per tile and the cluster's size: one token tile up to tn_max tokens,
-// and as many CTAs per tile as keep all of them on the SMs at once, each with
-// at least 4 reduction steps.
+// The geometry.  Without a split: one token tile up to tn = 256 tokens (gated:
+// 128, two accumulators).  Where the tiles leave SMs idle, the reduction is
+// split over the largest cluster whose clusters all fit on the GPU at once,
+// with at least 4 steps per CTA; the received partial sums then take up to 64
+// KB of the ring's room, so the token tile is at most half as wide.
 void fill(Args& a, int64_t T, int N, int64_t k, int segs, bool gated, int32_t* flags) {
-    const int tn_max = gated ? 128 : 256;
+    const int acc = gated ? 2 : 1, ft = cdiv(N, 128);
     a.T = (int)T;
     a.N = N;
-    const int tiles_t = cdiv(T, tn_max);
-    a.tn = cdiv(cdiv(T, tiles_t), 16) * 16;
     a.seg_steps = cdiv(k, kBK);
     a.steps = a.seg_steps * segs;
-    const int stage = (gated ? 2 : 1) * kABytes + a.tn * kBK * 2;
-    a.stages = std::min(kMaxStages, kRingBytes / stage);
-    const int64_t tiles = (int64_t)cdiv(N, 128) * cdiv(T, a.tn);
+    auto tile = [&](int most) { return cdiv(cdiv(T, cdiv(T, most)), 16) * 16; };
+    // clusters of s CTAs with 209 KB of shared memory each that a B200 holds at
+    // once (a cluster stays inside a GPC), a little below what it reports
+    static const int kFit[9] = {0, 148, 74, 44, 32, 26, 20, 0, 14};
     a.splits = 1;
-    while (a.splits < 8 && tiles * a.splits * 2 <= 2 * kDensePairs && a.steps / (a.splits * 2) >= 4) a.splits *= 2;
-    const uint32_t cols = (gated ? 2 : 1) * a.tn;
+    a.tn = tile(128 / acc);
+    const int64_t tiles = (int64_t)ft * cdiv(T, a.tn);
+    for (int s = 2; s <= 8; ++s)
+        if (tiles <= kFit[s] && a.steps >= 4 * s) a.splits = s;
+    if (a.splits == 1) a.tn = tile(256 / acc);
+    a.slice = cdiv(a.tn, a.splits);
+    const int stage = acc * kABytes + a.tn * kBK * 2;
+    const int recv = a.splits > 1 ? a.splits * acc * a.slice * kRowBytes : 0;
+    a.stages = std::min(kMaxStages, (kDataBytes - recv) / stage);
+    a.recv_off = a.stages * stage;
+    const uint32_t cols = acc * a.tn;
     a.tmem_cols = 32;
     while (a.tmem_cols < cols) a.tmem_cols *= 2;
     a.flags = flags;
@@ -273,22 +349,11 @@ cudaError_t launch(const CUtensorMap& A0, const CUtensorMap& A1, const CUtensorM
     auto* fn = dense_skinny_kernel<kGated, kAMN>;
     cudaError_t e = ensure_smem_attr(fn, kSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(cdiv(a.N, 128) * a.splits), (unsigned)cdiv(a.T, a.tn), 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)a.splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const dim3 grid((unsigned)(cdiv(a.N, 128) * a.splits), (unsigned)cdiv(a.T, a.tn), 1);
     trace_before(name, st);
-    e = cudaLaunchKernelEx(&cfg, fn, A0, A1, B0, B1, a);
+    e = launch_chained(fn, grid, kThreads, kSmem, a.splits, st, A0, A1, B0, B1, a);
     trace_after(st);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return e;
 }
 
 }  // namespace

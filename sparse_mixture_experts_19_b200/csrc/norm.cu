@@ -195,9 +195,12 @@ __global__ void __launch_bounds__(kThreads, 1) norm_fwd_kernel(const NormArgs a,
     if (g.t == 0) {
         for (int s = 0; s < geo.S; ++s) mbar_init(&bar[s], 1);
         fence_mbar_init();
+        chain_wait();
         for (int s = 0; s < geo.S; ++s)
             if (first + s * step < a.T) issue(first + s * step, s);
     }
+    chain_next();
+    chain_wait();
     g.sync();
     // the thread's columns of w and b stay in registers over all its rows
     float w[kVpt][8], b[kVpt][8];
@@ -287,9 +290,12 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormArgs a,
     if (g.t == 0) {
         for (int s = 0; s < geo.S; ++s) mbar_init(&bar[s], 1);
         fence_mbar_init();
+        chain_wait();
         for (int s = 0; s < geo.S; ++s)
             if (first + s * step < a.T) issue(first + s * step, s);
     }
+    chain_next();
+    chain_wait();
     g.sync();
     const float inv = 1.f / (float)a.H;
     float w[kVpt][8], dw[kVpt][8] = {}, db[kVpt][8] = {};
@@ -410,9 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormArgs a,
 
 // out[c] = sum over p < P of part[p * stride + c], in a fixed order: 32 rows
 // of threads take every 32nd partial each, then a tree over them.
-__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* __restrict__ part, int64_t stride, int P,
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, int64_t stride, int P,
                                                             int64_t second, int N, float* out0, float* out1) {
     __shared__ float s[32][33];
+    chain_next();
+    chain_wait();
     float* out = blockIdx.y ? out1 : out0;
     if (!out) return;
     const int c = blockIdx.x * 32 + threadIdx.x;
@@ -460,9 +468,9 @@ cudaError_t launch(Kernel k, const NormArgs& a, const Geo& g, const char* name, 
     cudaError_t e = ensure_smem_attr(k, kRingBytes);
     if (e != cudaSuccess) return e;
     trace_before(name, st);
-    k<<<blocks_of(a.T), kThreads, smem, st>>>(a, g);
+    e = launch_chained(k, blocks_of(a.T), kThreads, smem, 0, st, a, g);
     trace_after(st);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace
@@ -472,10 +480,10 @@ int norm_bwd_blocks(int64_t T) { return blocks_of(T); }
 cudaError_t launch_sum_partials(const float* part, int64_t stride, int P, int64_t second, int N, float* out0,
                                 float* out1, cudaStream_t st) {
     trace_before("sum_partials", st);
-    sum_partials_kernel<<<dim3((N + 31) / 32, out1 ? 2 : 1), dim3(32, 32), 0, st>>>(part, stride, P, second, N, out0,
-                                                                                   out1);
+    const cudaError_t e = launch_chained(sum_partials_kernel, dim3((N + 31) / 32, out1 ? 2 : 1), dim3(32, 32), 0, 0, st,
+                                         part, stride, P, second, N, out0, out1);
     trace_after(st);
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename X>

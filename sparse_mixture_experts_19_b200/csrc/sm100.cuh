@@ -57,6 +57,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return done != 0;
 }
 
+// Whether the phase of `parity` has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // Waits for the phase of `parity` to complete; false after kWaitLimit polls.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
     for (uint32_t i = 0; i < kWaitLimit; ++i)
@@ -120,6 +133,16 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(bar, parity); ++i) {
     }
 }
+
+// ------------------------------------------------- programmatic launches
+// A kernel launched by launch_chained (tma_host.cuh) may start while the one
+// before it on its stream still runs.  It sets itself up (barriers, TMEM,
+// tensor maps), then calls chain_wait before its first access to global
+// memory: that returns when the kernel before has completed and its writes are
+// visible.  chain_next lets the kernel after it start in the same way, once
+// every CTA of this one has called it.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
@@ -398,6 +421,20 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 // Every thread of both CTAs: release this CTA's prior writes, wait for the peer.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The two halves of cluster_sync, for work between them.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Bulk copy of `bytes` (a multiple of 16) from this CTA's shared memory to a
+// shared::cluster address, counted on the mbarrier at shared::cluster address
+// `bar` of the destination's CTA.
+__device__ __forceinline__ void bulk_push(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 // Address of the same shared-memory object in CTA `rank` of the cluster.

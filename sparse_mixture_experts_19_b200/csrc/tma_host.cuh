@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
+#include <utility>
 
 namespace moe {
 
@@ -156,6 +157,32 @@ inline cudaError_t ensure_smem_attr(Kernel kernel, size_t bytes) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess && n < 64) done[n++] = Done{fn, dev, bytes};
     return e;
+}
+
+// Launches a kernel whose set-up may overlap the end of the kernel before it
+// on the stream (programmatic stream serialization; the kernel calls
+// chain_wait).  cluster = 0: no cluster attribute (none, or the kernel's own).
+template <typename... P, typename... A>
+inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster,
+                                  cudaStream_t st, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (cluster > 0) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    cfg.attrs = attr;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 inline int device_sm_count() {
