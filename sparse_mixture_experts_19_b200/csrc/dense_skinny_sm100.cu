@@ -8,22 +8,23 @@
 // weight bytes.  A CTA owns one tile and one share of the reduction: a cluster
 // of S <= 8 CTAs splits the reduction (enough clusters to cover the SMs when
 // the output has few feature tiles), and each streams its share through a TMA
-// ring of up to 200 KB (weights 16 KB per 64-deep step, read once).  Then every
-// CTA pushes to CTA r, by bulk copies through distributed shared memory, its
-// partial sums of the r-th share of the tokens, and CTA r adds the S partials
-// in rank order and finishes them.  (Pulling them with loads from the peers
-// instead took 4 us of a 9 us call of 64 tokens: few loads in flight against
-// the latency of remote shared memory.)  The sum's order depends on the sizes
-// alone, so the bits do not change from run to run.
+// ring of up to 200 KB (weights 16 KB per 64-deep step, read once).  Then CTA r
+// of the cluster finishes the r-th share of the tokens: it adds the S partial
+// sums, its own and the peers' through distributed shared memory, all S loads
+// of an element in flight at once (one at a time they took 4 us of a 9 us call
+// of 64 tokens; pushing them instead, by bulk copies or by stores, was slower
+// from 128 tokens on).  CTA r starts at its own partial and goes round, so that
+// the peers are not all read in the same order; which CTA finishes a token
+// depends on the sizes alone, so the bits do not change from run to run.
 //
 //   forward: A = W rows K-major; gated: two A tiles (gate, up) and two
 //            accumulators per step
 //   input gradient: A = W read MN-major (features = W's columns), B = dz; the
 //            gated pair is one reduction over both (two segments)
 //
-// Six warps: TMA producer, MMA issuer, four that move the accumulator from
-// TMEM to shared memory; then all of them finish the elements (bias,
-// activation, residual).  Waits are bounded; no multicast loads.
+// Six warps: TMA producer, MMA issuer, four that move the accumulator out of
+// TMEM; then all of them finish the elements (bias, activation, residual).
+// Waits are bounded; no multicast loads.
 #include <algorithm>
 
 #include "act.cuh"
@@ -42,8 +43,8 @@ constexpr int kThreads = 192;
 constexpr int kABytes = 128 * kBK * 2;
 constexpr int kBox = 64 * kBK * 2;
 constexpr int kMaxStages = 12;
-constexpr int kDataBytes = 208 * 1024;  // ring, and the received partial sums behind it
-constexpr size_t kSmem = kDataBytes + 512 + 1024;
+constexpr int kRingBytes = 208 * 1024;
+constexpr size_t kSmem = kRingBytes + 512 + 1024;
 constexpr int kRowBytes = 128 * 4;  // one token's 128 features, float32
 
 struct Args {
@@ -52,8 +53,6 @@ struct Args {
     int stages;
     int seg_steps, steps;
     int splits;      // CTAs per cluster
-    int slice;       // splits > 1: most tokens one CTA of the cluster finishes
-    int recv_off;    // splits > 1: received partials [split][accumulator][slice][128]
     int act;
     const float* bias0;
     const float* bias1;
@@ -65,9 +64,9 @@ struct Args {
     int32_t* flags;
 };
 
-__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                  : "r"(addr)
                  : "memory");
@@ -88,11 +87,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
                                                                    const Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kDataBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes);
     uint64_t* empty = full + kMaxStages;
     uint64_t* done = empty + kMaxStages;
-    uint64_t* recv = done + 1;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(recv + 1);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -131,10 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
-        mbar_init(recv, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        if (a.splits > 1 && tk1 > tk0) mbar_arrive_expect_tx(recv, (uint32_t)(a.splits * kAcc * (tk1 - tk0) * kRowBytes));
         chain_wait();
         for (int s = 0; s < first; ++s) load_step(ks0 + s, s);
     }
@@ -148,7 +144,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    if (a.splits > 1) cluster_arrive();  // this CTA's barriers exist (waited for before the first push)
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
@@ -197,9 +192,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
             drain_wait(done, 0);
         }
     } else {
-        // ------------------------------------------------ TMEM -> partial tile in shared memory
-        // (the ring is free: the accumulator is complete, so every step's
-        // operands have been read).  part[accumulator][token][128 features]
+        // ------------------------------------------------ TMEM -> part[accumulator][token][128 features]
+        // (in the ring's place: the accumulator is complete, so every step's
+        // operands have been read)
         const int q = warp & 3;
         wait_sleep_or_abort(done, 0, abort_flag, a.flags);
         tc_fence_after();
@@ -213,41 +208,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
                 for (int i = 0; i < 16; ++i) part[(p * a.tn + c + i) * 128 + q * 32 + lane] = v[i];
             }
         tc_fence_before();
-        if (a.splits > 1) fence_async_smem();
     }
     __syncwarp();  // the single-lane roles join their warps
-    __syncthreads();
-    uint32_t src = smem_u32(smem);  // partial sums, and how they are laid out
-    int src_tok = 0, src_acc = a.tn * kRowBytes, src_rank = 0;
-    bool got = true;
-    if (a.splits > 1) {
-        cluster_wait();
-        if (warp == 0 && lane < a.splits) {
-            const int d0 = share(lane), d1 = share(lane + 1);
-            const uint32_t bar = mapa_shared(smem_u32(recv), lane);
-            const uint32_t dst = mapa_shared(src + a.recv_off, lane) + rank * kAcc * a.slice * kRowBytes;
-            if (d1 > d0)
-#pragma unroll
-                for (int p = 0; p < kAcc; ++p)
-                    bulk_push(dst + p * a.slice * kRowBytes, src + (p * a.tn + d0) * kRowBytes, (d1 - d0) * kRowBytes,
-                              bar);
-        }
-        __syncwarp();
-        if (tk1 > tk0) got = wait_sleep_or_abort(recv, 0, abort_flag, a.flags);
-        if (!got) drain_wait(recv, 0);
-        __syncwarp();
-        cluster_arrive();  // received: the senders' tiles are free (waited for before the exit)
-        src += a.recv_off;
-        src_tok = tk0;
-        src_acc = a.slice * kRowBytes;
-        src_rank = kAcc * a.slice * kRowBytes;
-    }
+    if (a.splits > 1)
+        cluster_sync();
+    else
+        __syncthreads();
 
     // ---------------------------------------------------- finish: 4 features of a token per thread
-    // and item, kItems items at once so that their loads are in flight together
-    constexpr int kItems = kGated ? 2 : 4;
+    // and token, kItems tokens at once so that their loads are in flight together
+    constexpr int kItems = 2;
+    const uint32_t part = smem_u32(smem) + lane * 16;
     const int f = lane * 4, n = n0 + f;  // a warp spans the tile's 128 features
-    if (got && n < a.N) {                // N is a multiple of 8
+    if (n < a.N) {                       // N is a multiple of 8
         float4 bias[kAcc];
 #pragma unroll
         for (int p = 0; p < kAcc; ++p) {
@@ -265,16 +238,33 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
 #pragma unroll
                 for (int p = 0; p < kAcc; ++p) s[u][p] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            for (int r = 0; r < a.splits; ++r) {
+            // four peers' loads at a time
+            for (int r0 = 0; r0 < a.splits; r0 += 4) {
+                float4 w[4][kItems][kAcc];
 #pragma unroll
-                for (int u = 0; u < kItems; ++u) {
-                    const int tok = min(tok0 + u * (kThreads / 32), tk1 - 1) - src_tok;
+                for (int r = 0; r < 4; ++r) {
+                    uint32_t peer = rank + r0 + r;
+                    if (peer >= (uint32_t)a.splits) peer -= a.splits;
+                    const bool in = r0 + r < a.splits;
+                    const uint32_t src = a.splits > 1 ? mapa_shared(part, in ? peer : rank) : part;
 #pragma unroll
-                    for (int p = 0; p < kAcc; ++p) {
-                        const float4 w = ld_shared_f4(src + r * src_rank + p * src_acc + tok * kRowBytes + f * 4);
-                        s[u][p].x += w.x, s[u][p].y += w.y, s[u][p].z += w.z, s[u][p].w += w.w;
-                    }
+                    for (int u = 0; u < kItems; ++u)
+#pragma unroll
+                        for (int p = 0; p < kAcc; ++p) {
+                            const int tok = min(tok0 + u * (kThreads / 32), tk1 - 1);
+                            w[r][u][p] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (in) w[r][u][p] = ld_cluster_f4(src + (p * a.tn + tok) * kRowBytes);
+                        }
                 }
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int u = 0; u < kItems; ++u)
+#pragma unroll
+                        for (int p = 0; p < kAcc; ++p) {
+                            s[u][p].x += w[r][u][p].x, s[u][p].y += w[r][u][p].y;
+                            s[u][p].z += w[r][u][p].z, s[u][p].w += w[r][u][p].w;
+                        }
             }
 #pragma unroll
             for (int u = 0; u < kItems; ++u) {
@@ -303,40 +293,32 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
         }
     }
     __syncwarp();
-    if (a.splits > 1) cluster_wait();  // every peer has received this CTA's partial sums
-    __syncthreads();
+    if (a.splits > 1) cluster_sync();  // the peers have read this CTA's partial sums
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, a.tmem_cols);
 }
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// The geometry.  Without a split: one token tile up to tn = 256 tokens (gated:
-// 128, two accumulators).  Where the tiles leave SMs idle, the reduction is
-// split over the largest cluster whose clusters all fit on the GPU at once,
-// with at least 4 steps per CTA; the received partial sums then take up to 64
-// KB of the ring's room, so the token tile is at most half as wide.
+// The geometry: token tiles of up to 256 tokens (gated: 128, two accumulators),
+// and, where the tiles leave SMs idle, the reduction split over the largest
+// cluster whose clusters all fit on the GPU at once, with at least 4 steps per
+// CTA.
 void fill(Args& a, int64_t T, int N, int64_t k, int segs, bool gated, int32_t* flags) {
-    const int acc = gated ? 2 : 1, ft = cdiv(N, 128);
+    const int acc = gated ? 2 : 1, most = 256 / acc;
     a.T = (int)T;
     a.N = N;
     a.seg_steps = cdiv(k, kBK);
     a.steps = a.seg_steps * segs;
-    auto tile = [&](int most) { return cdiv(cdiv(T, cdiv(T, most)), 16) * 16; };
+    a.tn = cdiv(cdiv(T, cdiv(T, most)), 16) * 16;
+    const int64_t tiles = (int64_t)cdiv(N, 128) * cdiv(T, a.tn);
     // clusters of s CTAs with 209 KB of shared memory each that a B200 holds at
     // once (a cluster stays inside a GPC), a little below what it reports
     static const int kFit[9] = {0, 148, 74, 44, 32, 26, 20, 0, 14};
     a.splits = 1;
-    a.tn = tile(128 / acc);
-    const int64_t tiles = (int64_t)ft * cdiv(T, a.tn);
     for (int s = 2; s <= 8; ++s)
         if (tiles <= kFit[s] && a.steps >= 4 * s) a.splits = s;
-    if (a.splits == 1) a.tn = tile(256 / acc);
-    a.slice = cdiv(a.tn, a.splits);
-    const int stage = acc * kABytes + a.tn * kBK * 2;
-    const int recv = a.splits > 1 ? a.splits * acc * a.slice * kRowBytes : 0;
-    a.stages = std::min(kMaxStages, (kDataBytes - recv) / stage);
-    a.recv_off = a.stages * stage;
+    a.stages = std::min(kMaxStages, kRingBytes / (acc * kABytes + a.tn * kBK * 2));
     const uint32_t cols = acc * a.tn;
     a.tmem_cols = 32;
     while (a.tmem_cols < cols) a.tmem_cols *= 2;
