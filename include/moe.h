@@ -525,9 +525,14 @@ typedef struct {
     int32_t grad_dtype; /* moe_dtype_t of the weight gradients                */
 } moe_dense_config_t;
 
-/* Workspaces of the four calls below: 256-byte aligned, starting with the
- * device check flags (zeroed before first use, read by
- * moe_dense_get_device_status); 0 for an invalid cfg (moe_last_error). */
+/* Workspaces of the four calls below: 256-byte aligned; 0 for an invalid cfg
+ * (moe_last_error).  The first MOE_DENSE_WS_HEADER bytes, device check flags
+ * and counters, must be zero before the workspace's first use; every call
+ * leaves the counters zero.  After a call whose flags
+ * (moe_dense_get_device_status) report a timeout, that query has cleared them
+ * again.  One workspace may serve calls of different sizes, one after the
+ * other. */
+#define MOE_DENSE_WS_HEADER 8448
 size_t moe_linear_workspace_size(const moe_dense_config_t* cfg);
 size_t moe_linear_backward_workspace_size(const moe_dense_config_t* cfg);
 size_t moe_gated_workspace_size(const moe_dense_config_t* cfg);
@@ -586,7 +591,8 @@ moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, c
                                 moe_stream_t stream);
 
 /* moe_get_device_status for a workspace of the moe_linear_* and moe_gated_*
- * calls: waits for `stream`, returns and clears its device check flags. */
+ * calls: waits for `stream`, returns and clears its device check flags (and,
+ * if any was set, its counters). */
 moe_status_t moe_dense_get_device_status(void* ws, size_t ws_bytes, moe_stream_t stream, int32_t* flags_out);
 
 /* Waits for `stream`, then returns the device check flags (MOE_DEVFLAG_*)

@@ -25,6 +25,7 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "M
 DEVFLAG_BAD_EXPERT_INDEX = 0x1
 DEVFLAG_WAIT_TIMEOUT = 0x2
 ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
+DENSE_WS_HEADER = 8448  # MOE_DENSE_WS_HEADER
 NORMS = {"layer": 0, "rms": 1}
 
 
@@ -489,11 +490,11 @@ def _sized(size_fn, cfg) -> int:
 
 
 def _new_ws(nbytes: int, device):
-    """A workspace whose device check flags (its first bytes) are clear."""
+    """A workspace whose header (device check flags, counters) is clear."""
     import torch
 
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    ws[:256].zero_()
+    ws[:DENSE_WS_HEADER].zero_()
     return ws
 
 

@@ -58,11 +58,6 @@ struct DenseDzArgs {
 int dense_dz_row_blocks(int64_t T, int64_t N);
 // dz (dg, du) and, where db0 / db1 are non-null, the bias gradients.
 cudaError_t launch_dense_dz(DenseDzArgs a, bool gated, int act, float* db0, float* db1, cudaStream_t st);
-// out0[i] = sum over s < S of part[s][0][i], out1 (nullable) of part[s][1][i];
-// n values each (a multiple of 4), float32 or bf16 outputs.
-cudaError_t launch_sum_splits(const float* part, int64_t n, int S, void* out0, void* out1, bool f32,
-                              cudaStream_t st);
-
 // ---- tensor-core products (operands bf16, row-major, float32 accumulators)
 struct DenseOut {
     int act;
@@ -74,16 +69,25 @@ struct DenseOut {
     bf16* z1;            // gated: u
 };
 
+// Workspace of one product.
+struct DenseWs {
+    int32_t* flags;
+    uint32_t* counters;  // zero between calls
+    float* part;         // the product's ..._part_floats
+};
+constexpr size_t kDenseCounterBytes = 8192;
+
 // y = act(x W^T + b) + res; gated (w1 non-null): y = act(x W0^T + b0) (x W1^T + b1).
+size_t dense_fwd_part_floats(int64_t T, int K, int N, bool gated);
 cudaError_t launch_dense_fwd(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
-                             const DenseOut& o, int32_t* flags, cudaStream_t st);
-// dx [T, K] = dz0 W0 (+ dz1 W1), dz [T, N], W [N, K].
+                             const DenseOut& o, const DenseWs& ws, cudaStream_t st);
+// dx [T, K] = dz0 W0 (+ dz1 W1), dz [T, N], W [N, K]; segs = 1 or 2 products.
+size_t dense_dgrad_part_floats(int64_t T, int K, int N, int segs);
 cudaError_t launch_dense_dgrad(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T, int K,
-                               int N, void* dx, int32_t* flags, cudaStream_t st);
-// dW_p [N, K] = dz_p^T x for one or two dz; part: scratch of
-// dense_wgrad_part_floats floats.
+                               int N, void* dx, const DenseWs& ws, cudaStream_t st);
+// dW_p [N, K] = dz_p^T x for one or two dz.
 size_t dense_wgrad_part_floats(int64_t T, int K, int N, int problems);
 cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, int64_t T, int K, int N, void* dw0,
-                               void* dw1, bool f32, float* part, int32_t* flags, cudaStream_t st);
+                               void* dw1, bool f32, const DenseWs& ws, cudaStream_t st);
 
 }  // namespace moe

@@ -4,6 +4,8 @@
 // moe_dense_get_device_status (documented to wait).
 #include <math.h>
 
+#include <algorithm>
+
 #include "abi_util.cuh"
 #include "dense.cuh"
 
@@ -45,11 +47,10 @@ moe_status_t check_dense(const moe_dense_config_t* c) {
 
 // Pieces of a dense workspace.
 struct DensePlan {
-    int32_t* flags;
+    DenseWs ws;  // flags and counters first: the header moe_dense_get_device_status clears
     bf16* dz0;   // [T, N], unless the linear layer has no activation
     bf16* dz1;   // gated
     float* sums; // partial bias gradients
-    float* part; // partial weight gradients
     size_t bytes;
 };
 
@@ -62,15 +63,21 @@ void make_dense_plan(const moe_dense_config_t* c, bool gated, bool backward, voi
         return r;
     };
     *p = DensePlan{};
-    p->flags = (int32_t*)take(64);
+    p->ws.flags = (int32_t*)take(64);
+    p->ws.counters = (uint32_t*)take(kDenseCounterBytes);
+    const int two = gated ? 2 : 1;
+    size_t part = 0;
     if (backward && c->T > 0) {
         const size_t tn = (size_t)c->T * c->N;
-        const int problems = gated ? 2 : 1;
         if (gated || c->act != MOE_ACT_NONE) p->dz0 = (bf16*)take(tn * 2);
         if (gated) p->dz1 = (bf16*)take(tn * 2);
-        p->sums = (float*)take(sizeof(float) * problems * c->N * dense_dz_row_blocks(c->T, c->N));
-        p->part = (float*)take(sizeof(float) * dense_wgrad_part_floats(c->T, c->K, c->N, problems));
+        p->sums = (float*)take(sizeof(float) * two * c->N * dense_dz_row_blocks(c->T, c->N));
+        // the two products run one after the other and share it
+        part = std::max(dense_dgrad_part_floats(c->T, c->K, c->N, two), dense_wgrad_part_floats(c->T, c->K, c->N, two));
+    } else if (c->T > 0) {
+        part = dense_fwd_part_floats(c->T, c->K, c->N, gated);
     }
+    p->ws.part = (float*)take(sizeof(float) * part);
     p->bytes = off;
 }
 
@@ -212,7 +219,7 @@ moe_status_t moe_linear_forward(const moe_dense_config_t* cfg, const void* x, co
     o.res = (const bf16*)residual;
     o.y = (bf16*)y;
     o.z0 = (bf16*)z_out;
-    CUDA_TRY(launch_dense_fwd(x, w, nullptr, cfg->T, cfg->K, cfg->N, o, p.flags, (cudaStream_t)stream), "linear_fwd");
+    CUDA_TRY(launch_dense_fwd(x, w, nullptr, cfg->T, cfg->K, cfg->N, o, p.ws, (cudaStream_t)stream), "linear_fwd");
     return MOE_OK;
 }
 
@@ -249,10 +256,10 @@ moe_status_t moe_linear_backward(const moe_dense_config_t* cfg, const void* dy, 
         a.part = p.sums;
         CUDA_TRY(launch_dense_dz(a, false, cfg->act, d_bias, nullptr, st), "linear_dz");
     }
-    if (dx) CUDA_TRY(launch_dense_dgrad(dz, nullptr, w, nullptr, cfg->T, cfg->K, cfg->N, dx, p.flags, st), "linear_dgrad");
+    if (dx) CUDA_TRY(launch_dense_dgrad(dz, nullptr, w, nullptr, cfg->T, cfg->K, cfg->N, dx, p.ws, st), "linear_dgrad");
     if (d_w)
         CUDA_TRY(launch_dense_wgrad(dz, nullptr, x, cfg->T, cfg->K, cfg->N, d_w, nullptr, cfg->grad_dtype == MOE_F32,
-                                    p.part, p.flags, st),
+                                    p.ws, st),
                  "linear_wgrad");
     return MOE_OK;
 }
@@ -285,7 +292,7 @@ moe_status_t moe_gated_forward(const moe_dense_config_t* cfg, const void* x, con
     o.y = (bf16*)h;
     o.z0 = (bf16*)g_out;
     o.z1 = (bf16*)u_out;
-    CUDA_TRY(launch_dense_fwd(x, w_gate, w_up, cfg->T, cfg->K, cfg->N, o, p.flags, (cudaStream_t)stream), "gated_fwd");
+    CUDA_TRY(launch_dense_fwd(x, w_gate, w_up, cfg->T, cfg->K, cfg->N, o, p.ws, (cudaStream_t)stream), "gated_fwd");
     return MOE_OK;
 }
 
@@ -331,11 +338,11 @@ moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, c
     a.part = p.sums;
     CUDA_TRY(launch_dense_dz(a, true, cfg->act, d_b_gate, d_b_up, st), "gated_dgu");
     if (dx)
-        CUDA_TRY(launch_dense_dgrad(p.dz0, p.dz1, w_gate, w_up, cfg->T, cfg->K, cfg->N, dx, p.flags, st),
+        CUDA_TRY(launch_dense_dgrad(p.dz0, p.dz1, w_gate, w_up, cfg->T, cfg->K, cfg->N, dx, p.ws, st),
                  "gated_dgrad");
     if (d_w_gate)
         CUDA_TRY(launch_dense_wgrad(p.dz0, p.dz1, x, cfg->T, cfg->K, cfg->N, d_w_gate, d_w_up,
-                                    cfg->grad_dtype == MOE_F32, p.part, p.flags, st),
+                                    cfg->grad_dtype == MOE_F32, p.ws, st),
                  "gated_wgrad");
     return MOE_OK;
 }
@@ -343,8 +350,14 @@ moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, c
 moe_status_t moe_dense_get_device_status(void* ws, size_t ws_bytes, moe_stream_t stream, int32_t* flags_out) {
     if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
     if ((uintptr_t)ws % kWsAlign) return fail(MOE_ERR_WORKSPACE, "workspace not %d-byte aligned", kWsAlign);
-    if (ws_bytes < kWsAlign) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %d", ws_bytes, kWsAlign);
-    return read_device_flags((int32_t*)ws, (cudaStream_t)stream, flags_out);
+    static_assert(MOE_DENSE_WS_HEADER == kWsAlign + kDenseCounterBytes, "workspace header");
+    if (ws_bytes < MOE_DENSE_WS_HEADER)
+        return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %d", ws_bytes, MOE_DENSE_WS_HEADER);
+    const moe_status_t s = read_device_flags((int32_t*)ws, (cudaStream_t)stream, flags_out);
+    // a call that gave up may have left its counters counting
+    if (s == MOE_ERR_DEVICE_CHECK)
+        CUDA_TRY(cudaMemsetAsync((char*)ws + kWsAlign, 0, kDenseCounterBytes, (cudaStream_t)stream), "counters clear");
+    return s;
 }
 
 }  // extern "C"

@@ -104,29 +104,6 @@ __global__ void __launch_bounds__(32 * kLanes) dense_dz_kernel(const DenseDzArgs
     }
 }
 
-// out[i] = sum over s < S of part[s * n + i], s in order, 4 per thread.
-template <typename O>
-__global__ void __launch_bounds__(256) sum_splits_kernel(const float* part, int64_t n, int S, int nout,
-                                                         O* out0, O* out1) {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    sm100::chain_next();
-    sm100::chain_wait();
-    if (i >= n) return;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < S; ++s) {
-        const float4 p = *reinterpret_cast<const float4*>(part + ((int64_t)s * nout + blockIdx.y) * n + i);
-        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
-    }
-    O* out = blockIdx.y ? out1 : out0;
-    if constexpr (sizeof(O) == 4) {
-        *reinterpret_cast<float4*>(out + i) = v;
-    } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-        *reinterpret_cast<uint2*>(out + i) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    }
-}
-
 }  // namespace
 
 // Row ranges: enough blocks to fill the GPU about 8 times over (2048 threads
@@ -154,18 +131,6 @@ cudaError_t launch_dense_dz(DenseDzArgs a, bool gated, int act, float* db0, floa
     if (e != cudaSuccess || !a.part) return e;
     const int per = gated ? 2 : 1;
     return launch_sum_partials(a.part, (int64_t)per * a.N, rb, a.N, a.N, db0, gated ? db1 : nullptr, st);
-}
-
-cudaError_t launch_sum_splits(const float* part, int64_t n, int S, void* out0, void* out1, bool f32,
-                              cudaStream_t st) {
-    const int nout = out1 ? 2 : 1;
-    const dim3 grid((unsigned)((n / 4 + 255) / 256), nout);
-    trace_before("sum_splits", st);
-    const cudaError_t e =
-        f32 ? launch_chained(sum_splits_kernel<float>, grid, 256, 0, 0, st, part, n, S, nout, (float*)out0, (float*)out1)
-            : launch_chained(sum_splits_kernel<bf16>, grid, 256, 0, 0, st, part, n, S, nout, (bf16*)out0, (bf16*)out1);
-    trace_after(st);
-    return e;
 }
 
 }  // namespace moe

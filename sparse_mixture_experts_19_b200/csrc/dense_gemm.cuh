@@ -11,9 +11,11 @@ namespace moe {
 // the sizes alone.
 constexpr int kDensePairs = 74;
 
+size_t dense_fwd_pairs_part_floats(int64_t T, int K, int N, bool gated);
+size_t dense_dgrad_pairs_part_floats(int64_t T, int K, int N, int segs);
 cudaError_t launch_dense_fwd_pairs(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
-                                   const DenseOut& o, int32_t* flags, cudaStream_t st);
+                                   const DenseOut& o, const DenseWs& ws, cudaStream_t st);
 cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T,
-                                     int K, int N, void* dx, int32_t* flags, cudaStream_t st);
+                                     int K, int N, void* dx, const DenseWs& ws, cudaStream_t st);
 
 }  // namespace moe

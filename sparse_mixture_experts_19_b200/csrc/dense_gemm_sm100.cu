@@ -11,7 +11,7 @@
 //   weight gradient dW = dz^T x (two problems for the gated pair): both MN-major
 //
 // One persistent kernel template on CTA pairs (cta_group::2): a tile is 256
-// rows x kBN columns, each CTA of the pair stages its own 128 rows of A and
+// rows x 256 columns (gated: 128 output columns, 256 accumulator columns), each CTA of the pair stages its own 128 rows of A and
 // half of B, and the leader issues M = 256 MMAs that read both CTAs' shared
 // memory: per CTA and 64-deep reduction step 32 KB arrive for 2 x 128 x 256 x
 // 64 flops, which keeps operand traffic below the tensor pipe's time.  A stage
@@ -20,6 +20,13 @@
 // were a fifth of the time.  TMEM holds two accumulators, so a tile's epilogue
 // overlaps the next tile's main loop.  Bound by the tensor pipe at large sizes, by the stores (weight
 // gradients of few tokens) or the operands' HBM reads otherwise.
+//
+// Tiles that do not fill the last wave of pairs are split along the reduction
+// (tail_plan): every split writes its float32 sums to the workspace, and the
+// one that arrives last at a tile's counter adds them in split order and runs
+// the epilogue.  Nothing waits for another CTA, and the order of the sum is
+// fixed.  The counters count warps' regions (32 rows x half the columns), so no
+// CTA-wide barrier is needed, and return to zero.
 //
 // Roles (10 warps): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
 // epilogue: warp w drains TMEM lanes 32 (w % 4) and one half of the columns.
@@ -55,57 +62,72 @@ constexpr int kEpiBytes = kEpiWarps * kEpiBuf;
 // What a tile's epilogue does.
 enum Mode { kLinear = 0, kGated = 1, kF32 = 2 };
 
-template <int kBN, int kMode>
-struct Cfg {
-    static constexpr int kBHalf = kMode == kGated ? 128 : kBN / 2;  // B rows each CTA stages
-    static constexpr int kMmaN = 2 * kBHalf;
-    static constexpr int kBBytes = kBHalf * kBK * 2;
-    static constexpr int kStepBytes = kABytes + kBBytes;  // one 64-deep step
-    static constexpr int kStageBytes = 2 * kStepBytes;    // a stage holds two
-    static constexpr int kStages = kBHalf == 128 ? 3 : 4;
-    static constexpr size_t kEpiOff = (size_t)kStages * kStageBytes;
-    static constexpr size_t kBarOff = kEpiOff + kEpiBytes;
-    static constexpr size_t kSmem = kBarOff + 512 + 1024;
-    static_assert(kSmem <= 227 * 1024, "shared memory");
-};
+constexpr int kBHalf = 128;                       // B rows each CTA stages
+constexpr int kMmaN = 2 * kBHalf;
+constexpr int kBBytes = kBHalf * kBK * 2;
+constexpr int kStepBytes = kABytes + kBBytes;     // one 64-deep step
+constexpr int kStageBytes = 2 * kStepBytes;       // a stage holds two
+constexpr int kStages = 3;
+constexpr size_t kEpiOff = (size_t)kStages * kStageBytes;
+constexpr size_t kBarOff = kEpiOff + kEpiBytes;
+constexpr size_t kSmem = kBarOff + 512 + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+// Output columns of a tile.
+template <int kMode>
+constexpr int tile_cols() { return kMode == kGated ? 128 : 256; }
 
 struct Args {
     int M, N;        // output rows and columns of one problem
-    int mt, nt;      // tiles of 256 rows, kBN columns
+    int mt, nt;      // its tiles
     int gm;          // row tiles per band
     int seg_steps;   // reduction steps of one segment
     int steps;       // reduction steps in all (segments x seg_steps)
-    int split_steps; // steps of one split (= steps when there is one)
-    int problems;    // 1 or 2: weight gradients that share B
-    int splits;      // > 1: partial sums to slice split * problems + problem of D0
-    int64_t total;
+    int full;        // tiles done whole
+    int splits;      // the others: each in this many units
+    int total;       // units: full + splits * (tiles - full)
     int act;
     const float* bias0;
     const float* bias1;
     bool has_res, has_z0, has_z1;
+    float* part;         // partial sums of the split tiles
+    uint32_t* counters;  // [split tiles][2 CTAs][8 warps]
     int32_t* flags;
 };
 
 struct Tile {
-    int m0, n0, prob, split, k0, k1;
+    int m0, n0, prob;
+    int k0, k1;        // reduction steps
+    int slot, split;   // slot >= 0: a unit of the slot-th split tile
 };
 
-// Tiles of one problem and split: bands of gm row tiles, the row tile running
-// fastest, so that pairs working side by side share B's columns and a band's A
-// rows stay in L2.
+// Unit t.  Tiles of one problem run in bands of gm row tiles, the row tile
+// running fastest, so that pairs working side by side share B's columns and a
+// band's A rows stay in L2.
 template <int kBN>
-__device__ __forceinline__ Tile decode(int64_t t, const Args& a) {
-    const int per = a.mt * a.nt;
-    const int z = (int)(t / per), local = (int)(t % per);
+__device__ __forceinline__ Tile decode(int t, const Args& a) {
+    Tile ti;
+    ti.slot = -1;
+    ti.split = 0;
+    ti.k0 = 0;
+    ti.k1 = a.steps;
+    if (t >= a.full) {
+        const int u = t - a.full;
+        const int slot = u / a.splits;
+        t = a.full + slot;
+        if (a.splits > 1) {
+            ti.slot = slot;
+            ti.split = u - slot * a.splits;
+            ti.k0 = (int)((int64_t)a.steps * ti.split / a.splits);
+            ti.k1 = (int)((int64_t)a.steps * (ti.split + 1) / a.splits);
+        }
+    }
+    const int per = a.mt * a.nt, local = t % per;
     const int band = local / (a.gm * a.nt), rem = local - band * a.gm * a.nt;
     const int first = band * a.gm, width = min(a.gm, a.mt - first);
-    Tile ti;
-    ti.prob = z % a.problems;
-    ti.split = z / a.problems;
+    ti.prob = t / per;
     ti.n0 = rem / width * kBN;
     ti.m0 = (first + rem % width) * (2 * kBM);
-    ti.k0 = ti.split * a.split_steps;
-    ti.k1 = min(ti.k0 + a.split_steps, a.steps);
     return ti;
 }
 
@@ -144,12 +166,12 @@ __device__ __forceinline__ void stage16(uint32_t buf, int lane, int sub, const u
         st_shared_u4(buf + buf_off(lane, 4 * sub + i), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
 }
 
-// The warp's staged buffer -> the map's box at (col, row, depth).
-__device__ __forceinline__ void store_buf(const CUtensorMap* map, uint32_t buf, int lane, int col, int row, int depth) {
+// The warp's staged buffer -> the map's box at (col, row).
+__device__ __forceinline__ void store_buf(const CUtensorMap* map, uint32_t buf, int lane, int col, int row) {
     fence_async_smem();
     __syncwarp();
     if (lane == 0) {
-        tma_store_3d(map, buf, col, row, depth);
+        tma_store_3d(map, buf, col, row, 0);
         bulk_commit();
     }
 }
@@ -160,18 +182,18 @@ __device__ __forceinline__ void buffer_free(int lane) {
     __syncwarp();
 }
 
-template <int kBN, int kMode, bool kAMN, bool kBMN>
+template <int kMode, bool kAMN, bool kBMN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_gemm_kernel(
     const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mA1,
     const __grid_constant__ CUtensorMap mB0, const __grid_constant__ CUtensorMap mB1,
     const __grid_constant__ CUtensorMap mD0, const __grid_constant__ CUtensorMap mD1,
     const __grid_constant__ CUtensorMap mD2, const __grid_constant__ CUtensorMap mR, const Args a) {
-    using C = Cfg<kBN, kMode>;
+    constexpr int kBN = tile_cols<kMode>();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // used in the leader
-    uint64_t* empty = full + C::kStages;
-    uint64_t* tfull = empty + C::kStages;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);  // used in the leader
+    uint64_t* empty = full + kStages;
+    uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 2;  // used in the leader: 8 epilogue warps x 2 CTAs
     uint64_t* drain = tempty + 2;
     uint64_t* rbar = drain + 1;  // residual chunks, one barrier per epilogue warp
@@ -182,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -208,27 +230,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     const uint32_t tmem_base = *tmem_holder;
     chain_next();
     chain_wait();
-    const int64_t pair = blockIdx.x / 2, npairs = gridDim.x / 2;
+    const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer (both CTAs)
         if (lane == 0) {
             uint32_t it = 0;
-            for (int64_t t = pair; t < a.total && !*abort_flag; t += npairs) {
+            for (int t = pair; t < a.total && !*abort_flag; t += npairs) {
                 const Tile ti = decode<kBN>(t, a);
                 const int arow = ti.m0 + (int)rank * kBM;
-                const int brow = kMode == kGated ? ti.n0 : ti.n0 + (int)rank * C::kBHalf;
+                const int brow = kMode == kGated ? ti.n0 : ti.n0 + (int)rank * kBHalf;
                 for (int ks = ti.k0, n; ks < ti.k1; ks += n, ++it) {
                     n = stage_steps(ks, ti, a);
-                    const int s = it % C::kStages;
-                    if (!wait_or_abort(&empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag, a.flags)) break;
+                    const int s = it % kStages;
+                    if (!wait_or_abort(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag, a.flags)) break;
                     const bool seg1 = ks >= a.seg_steps;
                     const CUtensorMap* pA = seg1 || ti.prob ? &mA1 : &mA0;
                     const CUtensorMap* pB = seg1 || (kMode == kGated && rank) ? &mB1 : &mB0;
-                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * n * C::kStepBytes);
+                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * n * kStepBytes);
                     for (int j = 0; j < n; ++j) {
                         const int kc = (ks + j - (seg1 ? a.seg_steps : 0)) * kBK;
-                        uint8_t* sa = smem + s * C::kStageBytes + j * C::kStepBytes;
+                        uint8_t* sa = smem + s * kStageBytes + j * kStepBytes;
                         uint8_t* sb = sa + kABytes;
                         if (kAMN) {
                             tma_load_3d_pair(sa, pA, &full[s], arow, kc, 0);
@@ -238,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                         }
                         if (kBMN) {
 #pragma unroll
-                            for (int i = 0; i < C::kBHalf / 64; ++i)
+                            for (int i = 0; i < kBHalf / 64; ++i)
                                 tma_load_3d_pair(sb + i * kBox, pB, &full[s], brow + 64 * i, kc, 0);
                         } else {
                             tma_load_3d_pair(sb, pB, &full[s], kc, brow, 0);
@@ -248,8 +270,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
             }
             // copies of both CTAs complete on the leader's barriers
             if (leader)
-                for (uint32_t j = (it > (uint32_t)C::kStages ? it - C::kStages : 0); j < it; ++j)
-                    drain_wait(&full[j % C::kStages], (j / C::kStages) & 1);
+                for (uint32_t j = (it > (uint32_t)kStages ? it - kStages : 0); j < it; ++j)
+                    drain_wait(&full[j % kStages], (j / kStages) & 1);
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader)
@@ -257,14 +279,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
         // short: descriptors by addition, the next step's barrier tested while
         // this step's MMAs are being issued.
         if (lane == 0 && leader) {
-            constexpr uint32_t kIdesc = idesc_bf16_major(2 * kBM, C::kMmaN, kAMN, kBMN);
+            constexpr uint32_t kIdesc = idesc_bf16_major(2 * kBM, kMmaN, kAMN, kBMN);
             constexpr uint32_t kStepA = (kAMN ? 2048 : 32) >> 4, kStepB = (kBMN ? 2048 : 32) >> 4;
             const uint32_t base = smem_u32(smem);
             const uint64_t da0 = kAMN ? desc_mnmajor_sw128(base, kBox, 1024) : desc_kmajor_sw128(base);
             const uint64_t db0 = kBMN ? desc_mnmajor_sw128(base + kABytes, kBox, 1024) : desc_kmajor_sw128(base + kABytes);
             uint32_t s = 0, ph = 0, tc = 0;
             bool ready = false;
-            for (int64_t t = pair; t < a.total && !*abort_flag; t += npairs, ++tc) {
+            for (int t = pair; t < a.total && !*abort_flag; t += npairs, ++tc) {
                 const Tile ti = decode<kBN>(t, a);
                 const uint32_t acc = tc & 1;
                 if (!wait_or_abort(&tempty[acc], ((tc >> 1) & 1) ^ 1, abort_flag, a.flags)) break;
@@ -280,13 +302,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                     }
                     tc_fence_after();
                     const uint32_t cur = s;
-                    if (++s == C::kStages) {
+                    if (++s == kStages) {
                         s = 0;
                         ph ^= 1;
                     }
                     ready = mbar_test(&full[s], ph);
-                    uint64_t da = da0 + cur * (C::kStageBytes >> 4), db = db0 + cur * (C::kStageBytes >> 4);
-                    for (int j = 0; j < n; ++j, da += C::kStepBytes >> 4, db += C::kStepBytes >> 4)
+                    uint64_t da = da0 + cur * (kStageBytes >> 4), db = db0 + cur * (kStageBytes >> 4);
+                    for (int j = 0; j < n; ++j, da += kStepBytes >> 4, db += kStepBytes >> 4)
 #pragma unroll
                         for (int kk = 0; kk < kBK / 16; ++kk) {
                             mma_bf16_pair(d, da + kk * kStepA, db + kk * kStepB, kIdesc, sum);
@@ -303,18 +325,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     } else {
         // ------------------------------------------------ epilogue (both CTAs)
         const int e = warp - 2, q = warp & 3, half = e >> 2;
-        uint8_t* buf_ptr = smem + C::kEpiOff + (size_t)e * kEpiBuf;
+        uint8_t* buf_ptr = smem + kEpiOff + (size_t)e * kEpiBuf;
         const uint32_t buf = smem_u32(buf_ptr);
-        constexpr int kHalfCols = (kMode == kGated ? 128 : kBN) / 2;  // output columns of this warp
-        constexpr int kChunk = kMode == kF32 ? 32 : 64;               // columns of the staging buffer
+        constexpr int kHalfCols = kBN / 2;               // output columns of this warp
+        constexpr int kChunk = kMode == kF32 ? 32 : 64;  // columns of the staging buffer
         constexpr int kChunks = kHalfCols / kChunk;
+        constexpr int kGroups = 4;  // this warp's accumulator columns, in groups of 32
         uint32_t tc = 0, rph = 0;
-        for (int64_t t = pair; t < a.total; t += npairs, ++tc) {
+        for (int t = pair; t < a.total; t += npairs, ++tc) {
             const Tile ti = decode<kBN>(t, a);
             const uint32_t acc = tc & 1;
             const int row = ti.m0 + (int)rank * kBM + q * 32;
             const int col0 = ti.n0 + half * kHalfCols;
-            const bool rows_in = row < a.M;
+            const bool in = row < a.M && col0 < a.N;
+            const bool whole = ti.slot < 0;
             // chunk j's residual into the staging buffer
             auto fetch_res = [&](int j) {
                 buffer_free(lane);
@@ -324,64 +348,125 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                 }
             };
             const bool res = kMode == kLinear && a.has_res;
-            const bool ahead = res && rows_in && col0 < a.N;
+            const bool ahead = res && in && whole;
             if (ahead) fetch_res(0);  // ahead of the accumulator
             if (!wait_sleep_or_abort(&tfull[acc], (tc >> 1) & 1, abort_flag, a.flags)) {
                 if (ahead) drain_wait(&rbar[e], rph);
                 break;
             }
             tc_fence_after();
-            const uint32_t tq = tmem_base + acc * kAccCols + ((uint32_t)(q * 32) << 16) + half * kHalfCols;
+            const uint32_t tq = tmem_base + acc * kAccCols + ((uint32_t)(q * 32) << 16);
+            // accumulator column of group g (gated: two groups of gate, two of up)
+            auto acc_col = [&](int g) {
+                return kMode == kGated ? (g >> 1) * 128 + half * 64 + (g & 1) * 32 : half * kHalfCols + g * 32;
+            };
             auto accumulator_free = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(&tempty[acc], 0);
             };
+            if (!in) {
+                accumulator_free();
+                continue;
+            }
+            if (!whole) {
+                // this split's sums of the warp's region, [group][8][lane]
+                // float4; the split that arrives last puts the sum over the
+                // splits, in order, back into TMEM and goes on as for a whole tile
+                constexpr int kRegion = kGroups * 8 * 32, kUnit = 2 * kEpiWarps * kRegion;
+                float4* parts = reinterpret_cast<float4*>(a.part) + (int64_t)ti.slot * a.splits * kUnit +
+                                (rank * kEpiWarps + e) * kRegion + lane;
+#pragma unroll 1
+                for (int g = 0; g < kGroups; ++g) {
+                    float v[32];
+                    tmem_ld32(tq + acc_col(g), v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        __stcg(parts + (int64_t)ti.split * kUnit + (g * 8 + i) * 32,
+                               make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                }
+                __threadfence();
+                __syncwarp();
+                uint32_t before = 0;
+                uint32_t* counter = a.counters + (ti.slot * 2 + rank) * kEpiWarps + e;
+                if (lane == 0) {
+                    before = atomicAdd(counter, 1u);
+                    if (before == (uint32_t)a.splits - 1) *counter = 0;  // for the next call
+                }
+                before = __shfl_sync(0xffffffffu, before, 0);
+                if (before != (uint32_t)a.splits - 1) {
+                    accumulator_free();
+                    continue;
+                }
+                __threadfence();
+#pragma unroll 1
+                for (int g = 0; g < kGroups; ++g) {
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 1
+                    for (int s = 0; s < a.splits; s += 2) {  // two splits' loads in flight
+                        const float4* p = parts + (int64_t)s * kUnit + g * 8 * 32;
+                        const bool two = s + 1 < a.splits;
+                        float4 w[2][8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[0][i] = __ldcg(p + i * 32);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            w[1][i] = two ? __ldcg(p + kUnit + i * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                v[4 * i] += w[h][i].x, v[4 * i + 1] += w[h][i].y;
+                                v[4 * i + 2] += w[h][i].z, v[4 * i + 3] += w[h][i].w;
+                            }
+                    }
+                    tmem_st32(tq + acc_col(g), v);
+                }
+                if (res) fetch_res(0);
+            }
+            auto sums = [&](int g, float (&v)[32], bool last) {
+                tmem_ld32(tq + acc_col(g), v);
+                if (last) accumulator_free();
+            };
             if (kMode == kF32) {
 #pragma unroll 1
                 for (int j = 0; j < kChunks; ++j) {
                     float v[32];
-                    tmem_ld32(tq + j * 32, v);
-                    if (j == kChunks - 1) accumulator_free();
+                    sums(j, v, j == kChunks - 1);
                     const int col = col0 + j * 32;
-                    if (!rows_in || col >= a.N) continue;
+                    if (col >= a.N) continue;
                     buffer_free(lane);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         st_shared_u4(buf + buf_off(lane, i), __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
                                      __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
-                    const bool parts = a.splits > 1;
-                    store_buf(!parts && ti.prob ? &mD1 : &mD0, buf, lane, col, row,
-                              parts ? ti.split * a.problems + ti.prob : 0);
+                    store_buf(ti.prob ? &mD1 : &mD0, buf, lane, col, row);
                 }
             } else if (kMode == kGated) {
-                const bool live = rows_in && col0 < a.N;
-                if (live) {
-                    // the kept projections first, one at a time through the buffer
+                // the kept projections first, one at a time through the buffer
 #pragma unroll 1
-                    for (int p = 0; p < 2; ++p) {
-                        if (!(p ? a.has_z1 : a.has_z0)) continue;
-                        buffer_free(lane);
+                for (int p = 0; p < 2; ++p) {
+                    if (!(p ? a.has_z1 : a.has_z0)) continue;
+                    buffer_free(lane);
 #pragma unroll
-                        for (int sub = 0; sub < 2; ++sub) {
-                            float v[32];
-                            tmem_ld32(tq + 128 * p + 32 * sub, v);
-                            add_bias(v, p ? a.bias1 : a.bias0, col0 + 32 * sub, a.N);
-                            uint32_t o[16];
-                            pack32(v, o);
-                            stage16(buf, lane, sub, o);
-                        }
-                        store_buf(p ? &mD2 : &mD1, buf, lane, col0, row, 0);
+                    for (int sub = 0; sub < 2; ++sub) {
+                        float v[32];
+                        sums(2 * p + sub, v, false);
+                        add_bias(v, p ? a.bias1 : a.bias0, col0 + 32 * sub, a.N);
+                        uint32_t o[16];
+                        pack32(v, o);
+                        stage16(buf, lane, sub, o);
                     }
+                    store_buf(p ? &mD2 : &mD1, buf, lane, col0, row);
                 }
                 uint32_t h[32];
 #pragma unroll
                 for (int sub = 0; sub < 2; ++sub) {
                     float g[32], u[32];
-                    tmem_ld32(tq + 32 * sub, g);
-                    tmem_ld32(tq + 128 + 32 * sub, u);
-                    if (sub == 1) accumulator_free();
-                    if (!live) continue;
+                    sums(sub, g, false);
+                    sums(2 + sub, u, sub == 1);
                     add_bias(g, a.bias0, col0 + 32 * sub, a.N);
                     add_bias(u, a.bias1, col0 + 32 * sub, a.N);
                     by_act(a.act, [&](auto k) {
@@ -390,17 +475,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                     });
                     pack32(g, h + 16 * sub);
                 }
-                if (live) {
-                    buffer_free(lane);
-                    stage16(buf, lane, 0, h);
-                    stage16(buf, lane, 1, h + 16);
-                    store_buf(&mD0, buf, lane, col0, row, 0);
-                }
+                buffer_free(lane);
+                stage16(buf, lane, 0, h);
+                stage16(buf, lane, 1, h + 16);
+                store_buf(&mD0, buf, lane, col0, row);
             } else {
 #pragma unroll 1
                 for (int j = 0; j < kChunks; ++j) {
                     const int col = col0 + j * kChunk;
-                    const bool live = rows_in && col < a.N;
+                    const bool live = col < a.N;
                     if (live) {
                         if (!res) {
                             buffer_free(lane);
@@ -414,8 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
 #pragma unroll
                     for (int sub = 0; sub < 2; ++sub) {
                         float v[32];
-                        tmem_ld32(tq + j * kChunk + 32 * sub, v);
-                        if (j == kChunks - 1 && sub == 1) accumulator_free();
+                        sums(2 * j + sub, v, j == kChunks - 1 && sub == 1);
                         if (!live) continue;
                         add_bias(v, a.bias0, col + 32 * sub, a.N);
                         uint32_t r[16];
@@ -444,12 +526,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                     }
                     if (live) {
                         if (a.has_z0) {
-                            store_buf(&mD1, buf, lane, col, row, 0);
+                            store_buf(&mD1, buf, lane, col, row);
                             buffer_free(lane);
                         }
                         stage16(buf, lane, 0, y);
                         stage16(buf, lane, 1, y + 16);
-                        store_buf(ti.prob ? &mD1 : &mD0, buf, lane, col, row, 0);
+                        store_buf(ti.prob ? &mD1 : &mD0, buf, lane, col, row);
                     }
                 }
             }
@@ -473,16 +555,14 @@ struct Maps {
     CUtensorMap A0, A1, B0, B1, D0, D1, D2, R;
 };
 
-template <int kBN, int kMode, bool kAMN, bool kBMN>
-cudaError_t launch(const Maps& m, Args a, const char* name, cudaStream_t st) {
-    using C = Cfg<kBN, kMode>;
-    auto* fn = dense_gemm_kernel<kBN, kMode, kAMN, kBMN>;
-    cudaError_t e = ensure_smem_attr(fn, C::kSmem);
+template <int kMode, bool kAMN, bool kBMN>
+cudaError_t launch(const Maps& m, const Args& a, const char* name, cudaStream_t st) {
+    auto* fn = dense_gemm_kernel<kMode, kAMN, kBMN>;
+    cudaError_t e = ensure_smem_attr(fn, kSmem);
     if (e != cudaSuccess) return e;
-    const int pairs = device_sm_count() / 2;
-    const int grid = 2 * (int)std::max<int64_t>(1, std::min<int64_t>(pairs, a.total));
+    const int grid = 2 * std::max(1, std::min(device_sm_count() / 2, a.total));
     trace_before(name, st);
-    e = launch_chained(fn, grid, kThreads, C::kSmem, 0, st, m.A0, m.A1, m.B0, m.B1, m.D0, m.D1, m.D2, m.R, a);
+    e = launch_chained(fn, grid, kThreads, kSmem, 0, st, m.A0, m.A1, m.B0, m.B1, m.D0, m.D1, m.D2, m.R, a);
     trace_after(st);
     return e;
 }
@@ -495,66 +575,108 @@ int band_of(int64_t k) {
     return (int)std::min<int64_t>(std::max<int64_t>(g, 8), 1 << 20);
 }
 
-// Column tile: 256, or 128 when its finer grid wins.  A 128-column tile takes
-// 0.82 of a 256-column tile's time (its 24 KB per reduction step against 32 KB
-// are bound by the loads; measured at T = 2048, 4096 -> 14336: 278 against 171
-// us), so it pays only where the last wave would leave most pairs idle.
-bool narrow_tiles(int64_t M, int64_t N, int64_t copies) {
-    const int64_t mt = cdiv(M, 2 * kBM) * copies;
-    const double wide = (double)cdiv(mt * cdiv(N, 256), kDensePairs);
-    const double narrow = (double)cdiv(mt * cdiv(N, 128), kDensePairs) * 0.82;
-    return narrow < wide;
+// Which tiles are split, and how.  Whole waves of kDensePairs tiles are done
+// whole; the r tiles of the last, partial wave in S units each where that ends
+// sooner: ceil(r S / pairs) rounds of steps / S reduction steps, plus what
+// writing the partial sums and adding S of them costs (L2 round trips of the
+// warps that arrive last).
+struct TailPlan {
+    int full, splits, slots;
+};
+constexpr int kSplitCost = 24, kSplitCostEach = 4;  // in steps of 64
+constexpr int kMaxSplits = 8;
+constexpr int kMaxSplitRounds = 3;  // bounds the workspace: 3 x 74 units of 256 KB
+TailPlan tail_plan(int64_t tiles, int steps) {
+    const int r = (int)(tiles % kDensePairs);
+    int best = 1, best_cost = steps;
+    for (int s = 2; s <= kMaxSplits && steps >= 4 * s; ++s) {
+        const int rounds = cdiv((int64_t)r * s, kDensePairs);
+        const int cost = rounds * (cdiv(steps, s) + kSplitCost + kSplitCostEach * s);
+        if (rounds <= kMaxSplitRounds && cost < best_cost) {
+            best = s;
+            best_cost = cost;
+        }
+    }
+    if (r == 0 || best == 1) return {(int)tiles, 1, 0};
+    return {(int)tiles - r, best, r};
 }
 
-void fill(Args& a, int64_t M, int N, int bn, int64_t k, int segs, int32_t* flags) {
-    a.M = (int)M;
-    a.N = N;
-    a.mt = cdiv(M, 2 * kBM);
-    a.nt = cdiv(N, bn);
-    a.gm = band_of(k * segs);
-    a.seg_steps = cdiv(k, kBK);
-    a.steps = a.seg_steps * segs;
-    a.split_steps = a.steps;
-    a.problems = a.splits = 1;
-    a.total = (int64_t)a.mt * a.nt;
-    a.flags = flags;
+constexpr int64_t kUnitFloats = 256 * 256;
+constexpr size_t kCounterBytes = (size_t)kDensePairs * 2 * kEpiWarps * sizeof(uint32_t);
+static_assert(kCounterBytes <= kDenseCounterBytes, "counters");
+
+struct Problem {  // M x N outputs over `steps` reduction steps, `problems` times
+    int64_t M;
+    int N, bn, seg_steps, segs, problems;
+    int64_t tiles() const { return (int64_t)cdiv(M, 2 * kBM) * cdiv(N, bn) * problems; }
+    TailPlan plan() const { return tail_plan(tiles(), seg_steps * segs); }
+    size_t part_floats() const {
+        const TailPlan p = plan();
+        return (size_t)p.slots * p.splits * kUnitFloats;
+    }
+};
+Problem fwd_problem(int64_t T, int K, int N, bool gated) { return {T, N, gated ? 128 : 256, cdiv(K, kBK), 1, 1}; }
+Problem dgrad_problem(int64_t T, int K, int N, int segs) { return {T, K, 256, cdiv(N, kBK), segs, 1}; }
+Problem wgrad_problem(int64_t T, int K, int N, int problems) { return {N, K, 256, cdiv(T, kBK), 1, problems}; }
+
+Args args_of(const Problem& pr, const DenseWs& ws) {
+    const TailPlan p = pr.plan();
+    Args a{};
+    a.M = (int)pr.M;
+    a.N = pr.N;
+    a.mt = cdiv(pr.M, 2 * kBM);
+    a.nt = cdiv(pr.N, pr.bn);
+    a.gm = band_of((int64_t)pr.seg_steps * pr.segs * kBK);
+    a.seg_steps = pr.seg_steps;
+    a.steps = pr.seg_steps * pr.segs;
+    a.full = p.full;
+    a.splits = p.splits;
+    a.total = p.full + p.slots * p.splits;
+    a.part = ws.part;
+    a.counters = ws.counters;
+    a.flags = ws.flags;
+    return a;
 }
 
 }  // namespace
 
+size_t dense_fwd_pairs_part_floats(int64_t T, int K, int N, bool gated) {
+    return fwd_problem(T, K, N, gated).part_floats();
+}
+size_t dense_dgrad_pairs_part_floats(int64_t T, int K, int N, int segs) {
+    return dgrad_problem(T, K, N, segs).part_floats();
+}
+size_t dense_wgrad_part_floats(int64_t T, int K, int N, int problems) {
+    return wgrad_problem(T, K, N, problems).part_floats();
+}
+
 cudaError_t launch_dense_fwd_pairs(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
-                                   const DenseOut& o, int32_t* flags, cudaStream_t st) {
+                                   const DenseOut& o, const DenseWs& ws, cudaStream_t st) {
     const bool gated = w1 != nullptr;
-    const bool narrow = !gated && narrow_tiles(T, N, 1);
-    const int bn = gated || narrow ? 128 : 256;
-    const int bhalf = narrow ? 64 : 128;
     Maps m;
-    bool ok = make_tile_map(&m.A0, false, x, K, T, 1, kBM) && make_tile_map(&m.B0, false, w0, K, N, 1, bhalf) &&
+    bool ok = make_tile_map(&m.A0, false, x, K, T, 1, kBM) && make_tile_map(&m.B0, false, w0, K, N, 1, kBHalf) &&
               make_tile_map(&m.D0, false, o.y, N, T, 1, 32);
     m.A1 = m.A0;
     m.B1 = m.B0;
     m.D1 = m.D2 = m.R = m.D0;
-    if (gated) ok = ok && make_tile_map(&m.B1, false, w1, K, N, 1, bhalf);
+    if (gated) ok = ok && make_tile_map(&m.B1, false, w1, K, N, 1, kBHalf);
     if (o.z0) ok = ok && make_tile_map(&m.D1, false, o.z0, N, T, 1, 32);
     if (o.z1) ok = ok && make_tile_map(&m.D2, false, o.z1, N, T, 1, 32);
     if (o.res) ok = ok && make_tile_map(&m.R, false, o.res, N, T, 1, 32);
     if (!ok) return cudaErrorInvalidValue;
-    Args a{};
-    fill(a, T, N, bn, K, 1, flags);
+    Args a = args_of(fwd_problem(T, K, N, gated), ws);
     a.act = o.act;
     a.bias0 = o.bias0;
     a.bias1 = o.bias1;
     a.has_res = o.res != nullptr;
     a.has_z0 = o.z0 != nullptr;
     a.has_z1 = o.z1 != nullptr;
-    if (gated) return launch<128, kGated, false, false>(m, a, "gated_fwd", st);
-    if (narrow) return launch<128, kLinear, false, false>(m, a, "linear_fwd", st);
-    return launch<256, kLinear, false, false>(m, a, "linear_fwd", st);
+    if (gated) return launch<kGated, false, false>(m, a, "gated_fwd", st);
+    return launch<kLinear, false, false>(m, a, "linear_fwd", st);
 }
 
 cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T,
-                                     int K, int N, void* dx, int32_t* flags, cudaStream_t st) {
-    const bool narrow = narrow_tiles(T, K, 1);
+                                     int K, int N, void* dx, const DenseWs& ws, cudaStream_t st) {
     Maps m;
     bool ok = make_tile_map(&m.A0, false, dz0, N, T, 1, kBM) && make_tile_map(&m.B0, false, w0, K, N, 1, 64) &&
               make_tile_map(&m.D0, false, dx, K, T, 1, 32);
@@ -564,62 +686,23 @@ cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const voi
     if (dz1)
         ok = ok && make_tile_map(&m.A1, false, dz1, N, T, 1, kBM) && make_tile_map(&m.B1, false, w1, K, N, 1, 64);
     if (!ok) return cudaErrorInvalidValue;
-    Args a{};
-    fill(a, T, K, narrow ? 128 : 256, N, dz1 ? 2 : 1, flags);
-    const char* name = dz1 ? "gated_dgrad" : "linear_dgrad";
-    if (narrow) return launch<128, kLinear, false, true>(m, a, name, st);
-    return launch<256, kLinear, false, true>(m, a, name, st);
-}
-
-// Splits of the weight gradient's reduction (the tokens): as many as fill the
-// pairs when the output has few tiles, each of at least 16 steps (1024 tokens).
-static int wgrad_splits(int64_t T, int K, int N, int problems) {
-    const int64_t tiles = (int64_t)cdiv(N, 256) * cdiv(K, 256) * problems;
-    const int64_t steps = cdiv(T, kBK);
-    const int64_t s = std::min<int64_t>(kDensePairs / tiles, steps / 16);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(s, 16));
-}
-
-size_t dense_wgrad_part_floats(int64_t T, int K, int N, int problems) {
-    const int s = wgrad_splits(T, K, N, problems);
-    return s > 1 ? (size_t)s * problems * N * K : 0;
+    const Args a = args_of(dgrad_problem(T, K, N, dz1 ? 2 : 1), ws);
+    return launch<kLinear, false, true>(m, a, dz1 ? "gated_dgrad" : "linear_dgrad", st);
 }
 
 cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, int64_t T, int K, int N, void* dw0,
-                               void* dw1, bool f32, float* part, int32_t* flags, cudaStream_t st) {
-    const int problems = dz1 ? 2 : 1;
-    const int splits = wgrad_splits(T, K, N, problems);
-    const bool parts = splits > 1;
-    const bool out32 = f32 || parts;
+                               void* dw1, bool f32, const DenseWs& ws, cudaStream_t st) {
     Maps m;
-    bool ok = make_tile_map(&m.A0, false, dz0, N, T, 1, 64) && make_tile_map(&m.B0, false, x, K, T, 1, 64);
-    if (parts)
-        ok = ok && make_tile_map(&m.D0, true, part, K, N, (uint64_t)splits * problems, 32);
-    else
-        ok = ok && make_tile_map(&m.D0, f32, dw0, K, N, 1, 32);
+    bool ok = make_tile_map(&m.A0, false, dz0, N, T, 1, 64) && make_tile_map(&m.B0, false, x, K, T, 1, 64) &&
+              make_tile_map(&m.D0, f32, dw0, K, N, 1, 32);
     m.A1 = m.A0;
     m.B1 = m.B0;
     m.D1 = m.D2 = m.R = m.D0;
-    if (dz1) {
-        ok = ok && make_tile_map(&m.A1, false, dz1, N, T, 1, 64);
-        if (!parts) ok = ok && make_tile_map(&m.D1, f32, dw1, K, N, 1, 32);
-    }
+    if (dz1) ok = ok && make_tile_map(&m.A1, false, dz1, N, T, 1, 64) && make_tile_map(&m.D1, f32, dw1, K, N, 1, 32);
     if (!ok) return cudaErrorInvalidValue;
-    const bool narrow = !parts && narrow_tiles(N, K, problems);
-    Args a{};
-    fill(a, N, K, narrow ? 128 : 256, T, 1, flags);
-    a.problems = problems;
-    a.splits = splits;
-    a.split_steps = cdiv(a.steps, splits);
-    a.total *= (int64_t)problems * splits;
+    const Args a = args_of(wgrad_problem(T, K, N, dz1 ? 2 : 1), ws);
     const char* name = dz1 ? "gated_wgrad" : "linear_wgrad";
-    cudaError_t e;
-    if (out32)
-        e = narrow ? launch<128, kF32, true, true>(m, a, name, st) : launch<256, kF32, true, true>(m, a, name, st);
-    else
-        e = narrow ? launch<128, kLinear, true, true>(m, a, name, st) : launch<256, kLinear, true, true>(m, a, name, st);
-    if (e != cudaSuccess || !parts) return e;
-    return launch_sum_splits(part, (int64_t)N * K, splits, dw0, dw1, f32, st);
+    return f32 ? launch<kF32, true, true>(m, a, name, st) : launch<kLinear, true, true>(m, a, name, st);
 }
 
 }  // namespace moe

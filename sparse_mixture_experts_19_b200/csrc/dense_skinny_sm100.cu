@@ -379,16 +379,23 @@ cudaError_t launch_dense_dgrad_skinny(const void* dz0, const void* dz1, const vo
 // the pair kernel's 256-row tiles.
 static bool skinny(int64_t T) { return T <= 256; }
 
+size_t dense_fwd_part_floats(int64_t T, int K, int N, bool gated) {
+    return skinny(T) ? 0 : dense_fwd_pairs_part_floats(T, K, N, gated);
+}
+size_t dense_dgrad_part_floats(int64_t T, int K, int N, int segs) {
+    return skinny(T) ? 0 : dense_dgrad_pairs_part_floats(T, K, N, segs);
+}
+
 cudaError_t launch_dense_fwd(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
-                             const DenseOut& o, int32_t* flags, cudaStream_t st) {
-    return skinny(T) ? launch_dense_fwd_skinny(x, w0, w1, T, K, N, o, flags, st)
-                     : launch_dense_fwd_pairs(x, w0, w1, T, K, N, o, flags, st);
+                             const DenseOut& o, const DenseWs& ws, cudaStream_t st) {
+    return skinny(T) ? launch_dense_fwd_skinny(x, w0, w1, T, K, N, o, ws.flags, st)
+                     : launch_dense_fwd_pairs(x, w0, w1, T, K, N, o, ws, st);
 }
 
 cudaError_t launch_dense_dgrad(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T, int K,
-                               int N, void* dx, int32_t* flags, cudaStream_t st) {
-    return skinny(T) ? launch_dense_dgrad_skinny(dz0, dz1, w0, w1, T, K, N, dx, flags, st)
-                     : launch_dense_dgrad_pairs(dz0, dz1, w0, w1, T, K, N, dx, flags, st);
+                               int N, void* dx, const DenseWs& ws, cudaStream_t st) {
+    return skinny(T) ? launch_dense_dgrad_skinny(dz0, dz1, w0, w1, T, K, N, dx, ws.flags, st)
+                     : launch_dense_dgrad_pairs(dz0, dz1, w0, w1, T, K, N, dx, ws, st);
 }
 
 }  // namespace moe

@@ -67,7 +67,7 @@ def test_null_configuration(lib):
 def test_workspaces(lib):
     r = ctypes.byref(dense())
     n = lib.moe_gated_backward_workspace_size(r)
-    assert n > lib.moe_gated_workspace_size(r) >= 256
+    assert n > lib.moe_gated_workspace_size(r) >= moe.DENSE_WS_HEADER
     args = [P, P, P, P, P, P, 2 * P, 3 * P, 4 * P, None, None]
     assert lib.moe_gated_backward(r, *args, None, n, None) == 3
     assert lib.moe_gated_backward(r, *args, P + 16, n, None) == 3
@@ -76,10 +76,10 @@ def test_workspaces(lib):
     m = lib.moe_norm_workspace_size(nr)
     assert lib.moe_norm_backward(nr, P, P, None, P, P, None, 2 * P, P, None, P, m - 1, None) == 3
     assert lib.moe_dense_get_device_status(None, 256, None, None) == 3
-    assert lib.moe_dense_get_device_status(P, 128, None, None) == 3
+    assert lib.moe_dense_get_device_status(P, moe.DENSE_WS_HEADER - 1, None, None) == 3
     # the workspace grows with T only as its contents do
     sizes = [moe.moe_linear_backward_workspace_size(moe.dense_config(t, 64, 32, "silu")) for t in (0, 1, 64, 4096)]
-    assert sizes == sorted(sizes) and sizes[0] == 256
+    assert sizes == sorted(sizes) and sizes[0] == moe.DENSE_WS_HEADER
 
 
 def test_linear_pointers(lib):

@@ -188,10 +188,10 @@ def test_norm_in_place_and_constant_rows(gpu_lib):
 
 
 # ----------------------------------------------------------------- linear
-# rows from one to several 256-row tiles, ragged K and N, both column tiles
-# (2200 x 2040: the wide one), the few-row kernel's split and unsplit clusters
+# rows from one to several 256-row tiles, ragged K and N, more tiles than pairs
+# (4000 x 1288), split and whole tiles, the few-row kernel's split and unsplit clusters
 LIN = [(1, 64, 8), (1, 4096, 264), (5, 72, 136), (16, 520, 128), (17, 2048, 520), (129, 200, 1032), (256, 72, 264),
-       (257, 1032, 264), (300, 8, 520), (513, 64, 72), (700, 328, 1000), (2200, 72, 2040)]
+       (257, 1032, 264), (300, 8, 520), (513, 64, 72), (700, 328, 1000), (2200, 72, 2040), (4000, 648, 1288)]
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -307,7 +307,7 @@ def test_gated_forward(gpu_lib, T, K, N, act):
 
 
 GATED_BWD = [(1, 64, 8, "silu"), (3, 4096, 264, "silu"), (65, 264, 72, "gelu"), (256, 136, 520, "relu"),
-             (257, 264, 136, "silu"), (300, 2040, 72, "gelu_tanh"), (72, 1032, 2200, "none"), (2100, 200, 328, "silu"),
+             (257, 264, 136, "silu"), (300, 72, 1000, "silu"), (300, 2040, 72, "gelu_tanh"), (72, 1032, 2200, "none"), (2100, 200, 328, "silu"),
              (4200, 72, 136, "silu")]
 
 
