@@ -582,6 +582,7 @@ int band_of(int64_t k) {
 // warps that arrive last).
 struct TailPlan {
     int full, splits, slots;
+    int cost;  // of the last wave, in steps
 };
 constexpr int kSplitCost = 24, kSplitCostEach = 4;  // in steps of 64
 constexpr int kMaxSplits = 8;
@@ -597,8 +598,9 @@ TailPlan tail_plan(int64_t tiles, int steps) {
             best_cost = cost;
         }
     }
-    if (r == 0 || best == 1) return {(int)tiles, 1, 0};
-    return {(int)tiles - r, best, r};
+    if (r == 0) return {(int)tiles, 1, 0, 0};
+    if (best == 1) return {(int)tiles, 1, 0, steps};
+    return {(int)tiles - r, best, r, best_cost};
 }
 
 constexpr int64_t kUnitFloats = 256 * 256;
@@ -640,6 +642,10 @@ Args args_of(const Problem& pr, const DenseWs& ws) {
 
 }  // namespace
 
+double dense_pairs_steps(int64_t T, int N, int64_t k, int segs, bool gated) {
+    const Problem p{T, N, gated ? 128 : 256, cdiv(k, kBK), segs, 1};
+    return (double)(p.tiles() / kDensePairs) * p.seg_steps * segs + p.plan().cost;
+}
 size_t dense_fwd_pairs_part_floats(int64_t T, int K, int N, bool gated) {
     return fwd_problem(T, K, N, gated).part_floats();
 }

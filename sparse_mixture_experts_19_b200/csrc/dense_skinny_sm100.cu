@@ -22,9 +22,10 @@
 //   input gradient: A = W read MN-major (features = W's columns), B = dz; the
 //            gated pair is one reduction over both (two segments)
 //
-// Six warps: TMA producer, MMA issuer, four that move the accumulator out of
-// TMEM; then all of them finish the elements (bias, activation, residual).
-// Waits are bounded; no multicast loads.
+// Twelve warps: TMA producer, MMA issuer, eight that move the accumulator from
+// TMEM to shared memory; then all of them finish the elements (bias,
+// activation, residual), which waits on loads and wants many warps.  Waits are
+// bounded; no multicast loads.
 #include <algorithm>
 
 #include "act.cuh"
@@ -39,7 +40,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kBK = 64;
-constexpr int kThreads = 192;
+constexpr int kThreads = 384;
 constexpr int kABytes = 128 * kBK * 2;
 constexpr int kBox = 64 * kBK * 2;
 constexpr int kMaxStages = 12;
@@ -191,17 +192,17 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
             mma_commit(done);
             drain_wait(done, 0);
         }
-    } else {
+    } else if (warp < 10) {
         // ------------------------------------------------ TMEM -> part[accumulator][token][128 features]
         // (in the ring's place: the accumulator is complete, so every step's
         // operands have been read)
-        const int q = warp & 3;
+        const int q = warp & 3, half = (warp - 2) >> 2;  // lanes, every second group of 16 columns
         wait_sleep_or_abort(done, 0, abort_flag, a.flags);
         tc_fence_after();
         float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int p = 0; p < kAcc; ++p)
-            for (int c = 0; c < tokens; c += 16) {
+            for (int c = 16 * half; c < tokens; c += 32) {
                 float v[16];
                 tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + p * a.tn + c, v);
 #pragma unroll
@@ -375,26 +376,48 @@ cudaError_t launch_dense_dgrad_skinny(const void* dz0, const void* dz1, const vo
     return launch<false, true>(A0, A1, B0, B1, a, dz1 ? "gated_dgrad_skinny" : "linear_dgrad_skinny", st);
 }
 
-// Few rows: the weights are streamed once and the SMs wait for HBM; many rows:
-// the pair kernel's 256-row tiles.
-static bool skinny(int64_t T) { return T <= 256; }
+// Which form a product of T rows, N outputs and a reduction of k (in `segs`
+// segments) takes: the one whose estimated time is less.  Both estimates are
+// fits to measurements of both forms at T = 1 ... 1024 on 2880 -> 2880, 4096 ->
+// 14336 and 2048 -> 768 (within 15%), in microseconds:
+//   few rows:  5 + 0.016 per token and accumulator (moving and adding the
+//              partial sums) + the rounds of CTAs x their steps, a step being
+//              the slower of its MMAs and its bytes at the 13 TB/s that the SMs
+//              draw from L2 together;
+//   pairs:     6 + 0.33 per reduction step of the rounds of tiles;
+// and neither reads its operands faster than 6.2 TB/s from HBM.  At T = 128 the
+// few-row form takes 10.0 against 20.4 us on 2880 -> 2880 (pairs: 12 tiles for
+// 74 pairs); at T = 256 it takes 39.7 against 31.6 us on 4096 -> 14336, where
+// 112 feature tiles read the tokens 112 times.
+static bool skinny(int64_t T, int N, int64_t k, int segs, bool gated) {
+    Args a{};
+    fill(a, T, N, k, segs, gated, nullptr);
+    const int acc = gated ? 2 : 1;
+    const double hbm = (acc * segs * (double)N * k + (double)T * k * segs) * 2 / 6.2e6;
+    const int64_t token_tiles = cdiv(T, a.tn), ctas = cdiv(N, 128) * token_tiles * a.splits;
+    const double at_once = (double)std::min<int64_t>(ctas, 148);
+    const double step = std::max(0.0011 * a.tn * acc, (acc * kABytes + a.tn * kBK * 2) * at_once / 13e6);
+    const double few = 5 + 0.016 * a.tn * acc + std::max(hbm, (double)cdiv(ctas, 148) * a.steps / a.splits * step);
+    const double pairs = 6 + std::max(hbm, 0.33 * dense_pairs_steps(T, N, k, segs, gated));
+    return few < pairs;
+}
 
 size_t dense_fwd_part_floats(int64_t T, int K, int N, bool gated) {
-    return skinny(T) ? 0 : dense_fwd_pairs_part_floats(T, K, N, gated);
+    return skinny(T, N, K, 1, gated) ? 0 : dense_fwd_pairs_part_floats(T, K, N, gated);
 }
 size_t dense_dgrad_part_floats(int64_t T, int K, int N, int segs) {
-    return skinny(T) ? 0 : dense_dgrad_pairs_part_floats(T, K, N, segs);
+    return skinny(T, K, N, segs, false) ? 0 : dense_dgrad_pairs_part_floats(T, K, N, segs);
 }
 
 cudaError_t launch_dense_fwd(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
                              const DenseOut& o, const DenseWs& ws, cudaStream_t st) {
-    return skinny(T) ? launch_dense_fwd_skinny(x, w0, w1, T, K, N, o, ws.flags, st)
+    return skinny(T, N, K, 1, w1 != nullptr) ? launch_dense_fwd_skinny(x, w0, w1, T, K, N, o, ws.flags, st)
                      : launch_dense_fwd_pairs(x, w0, w1, T, K, N, o, ws, st);
 }
 
 cudaError_t launch_dense_dgrad(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T, int K,
                                int N, void* dx, const DenseWs& ws, cudaStream_t st) {
-    return skinny(T) ? launch_dense_dgrad_skinny(dz0, dz1, w0, w1, T, K, N, dx, ws.flags, st)
+    return skinny(T, K, N, dz1 ? 2 : 1, false) ? launch_dense_dgrad_skinny(dz0, dz1, w0, w1, T, K, N, dx, ws.flags, st)
                      : launch_dense_dgrad_pairs(dz0, dz1, w0, w1, T, K, N, dx, ws, st);
 }
 
