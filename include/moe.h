@@ -532,7 +532,7 @@ typedef struct {
  * (moe_dense_get_device_status) report a timeout, that query has cleared them
  * again.  One workspace may serve calls of different sizes, one after the
  * other. */
-#define MOE_DENSE_WS_HEADER 8448
+#define MOE_DENSE_WS_HEADER 9984
 size_t moe_linear_workspace_size(const moe_dense_config_t* cfg);
 size_t moe_linear_backward_workspace_size(const moe_dense_config_t* cfg);
 size_t moe_gated_workspace_size(const moe_dense_config_t* cfg);

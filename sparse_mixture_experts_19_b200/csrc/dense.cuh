@@ -75,7 +75,7 @@ struct DenseWs {
     uint32_t* counters;  // zero between calls
     float* part;         // the product's ..._part_floats
 };
-constexpr size_t kDenseCounterBytes = 8192;
+constexpr size_t kDenseCounterBytes = 4864;  // of one product
 
 // y = act(x W^T + b) + res; gated (w1 non-null): y = act(x W0^T + b0) (x W1^T + b1).
 size_t dense_fwd_part_floats(int64_t T, int K, int N, bool gated);
@@ -85,9 +85,13 @@ cudaError_t launch_dense_fwd(const void* x, const void* w0, const void* w1, int6
 size_t dense_dgrad_part_floats(int64_t T, int K, int N, int segs);
 cudaError_t launch_dense_dgrad(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T, int K,
                                int N, void* dx, const DenseWs& ws, cudaStream_t st);
-// dW_p [N, K] = dz_p^T x for one or two dz.
+// Whether that leaves SMs for the weight gradient to run beside it.
+bool dense_dgrad_leaves_room(int64_t T, int K, int N, int segs);
+// dW_p [N, K] = dz_p^T x for one or two dz.  beside: the kernel before it on the
+// stream is launch_dense_dgrad of the same dz with another workspace's partial
+// sums and counters; the two may then run side by side.
 size_t dense_wgrad_part_floats(int64_t T, int K, int N, int problems);
 cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, int64_t T, int K, int N, void* dw0,
-                               void* dw1, bool f32, const DenseWs& ws, cudaStream_t st);
+                               void* dw1, bool f32, bool beside, const DenseWs& ws, cudaStream_t st);
 
 }  // namespace moe

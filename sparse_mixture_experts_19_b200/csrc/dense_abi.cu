@@ -47,7 +47,10 @@ moe_status_t check_dense(const moe_dense_config_t* c) {
 
 // Pieces of a dense workspace.
 struct DensePlan {
-    DenseWs ws;  // flags and counters first: the header moe_dense_get_device_status clears
+    // flags and both products' counters first: the header that
+    // moe_dense_get_device_status clears
+    DenseWs ws;   // the forward product, or the input gradient
+    DenseWs wws;  // the weight gradient
     bf16* dz0;   // [T, N], unless the linear layer has no activation
     bf16* dz1;   // gated
     float* sums; // partial bias gradients
@@ -65,19 +68,19 @@ void make_dense_plan(const moe_dense_config_t* c, bool gated, bool backward, voi
     *p = DensePlan{};
     p->ws.flags = (int32_t*)take(64);
     p->ws.counters = (uint32_t*)take(kDenseCounterBytes);
+    p->wws.flags = p->ws.flags;
+    p->wws.counters = (uint32_t*)take(kDenseCounterBytes);
     const int two = gated ? 2 : 1;
-    size_t part = 0;
     if (backward && c->T > 0) {
         const size_t tn = (size_t)c->T * c->N;
         if (gated || c->act != MOE_ACT_NONE) p->dz0 = (bf16*)take(tn * 2);
         if (gated) p->dz1 = (bf16*)take(tn * 2);
         p->sums = (float*)take(sizeof(float) * two * c->N * dense_dz_row_blocks(c->T, c->N));
-        // the two products run one after the other and share it
-        part = std::max(dense_dgrad_part_floats(c->T, c->K, c->N, two), dense_wgrad_part_floats(c->T, c->K, c->N, two));
+        p->ws.part = (float*)take(sizeof(float) * dense_dgrad_part_floats(c->T, c->K, c->N, two));
+        p->wws.part = (float*)take(sizeof(float) * dense_wgrad_part_floats(c->T, c->K, c->N, two));
     } else if (c->T > 0) {
-        part = dense_fwd_part_floats(c->T, c->K, c->N, gated);
+        p->ws.part = (float*)take(sizeof(float) * dense_fwd_part_floats(c->T, c->K, c->N, gated));
     }
-    p->ws.part = (float*)take(sizeof(float) * part);
     p->bytes = off;
 }
 
@@ -259,7 +262,7 @@ moe_status_t moe_linear_backward(const moe_dense_config_t* cfg, const void* dy, 
     if (dx) CUDA_TRY(launch_dense_dgrad(dz, nullptr, w, nullptr, cfg->T, cfg->K, cfg->N, dx, p.ws, st), "linear_dgrad");
     if (d_w)
         CUDA_TRY(launch_dense_wgrad(dz, nullptr, x, cfg->T, cfg->K, cfg->N, d_w, nullptr, cfg->grad_dtype == MOE_F32,
-                                    p.ws, st),
+                                    dx && dense_dgrad_leaves_room(cfg->T, cfg->K, cfg->N, 1), p.wws, st),
                  "linear_wgrad");
     return MOE_OK;
 }
@@ -342,7 +345,8 @@ moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, c
                  "gated_dgrad");
     if (d_w_gate)
         CUDA_TRY(launch_dense_wgrad(p.dz0, p.dz1, x, cfg->T, cfg->K, cfg->N, d_w_gate, d_w_up,
-                                    cfg->grad_dtype == MOE_F32, p.ws, st),
+                                    cfg->grad_dtype == MOE_F32,
+                                    dx && dense_dgrad_leaves_room(cfg->T, cfg->K, cfg->N, 2), p.wws, st),
                  "gated_wgrad");
     return MOE_OK;
 }
@@ -350,13 +354,13 @@ moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, c
 moe_status_t moe_dense_get_device_status(void* ws, size_t ws_bytes, moe_stream_t stream, int32_t* flags_out) {
     if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
     if ((uintptr_t)ws % kWsAlign) return fail(MOE_ERR_WORKSPACE, "workspace not %d-byte aligned", kWsAlign);
-    static_assert(MOE_DENSE_WS_HEADER == kWsAlign + kDenseCounterBytes, "workspace header");
+    static_assert(MOE_DENSE_WS_HEADER == kWsAlign + 2 * kDenseCounterBytes, "workspace header");
     if (ws_bytes < MOE_DENSE_WS_HEADER)
         return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %d", ws_bytes, MOE_DENSE_WS_HEADER);
     const moe_status_t s = read_device_flags((int32_t*)ws, (cudaStream_t)stream, flags_out);
     // a call that gave up may have left its counters counting
     if (s == MOE_ERR_DEVICE_CHECK)
-        CUDA_TRY(cudaMemsetAsync((char*)ws + kWsAlign, 0, kDenseCounterBytes, (cudaStream_t)stream), "counters clear");
+        CUDA_TRY(cudaMemsetAsync((char*)ws + kWsAlign, 0, 2 * kDenseCounterBytes, (cudaStream_t)stream), "counters clear");
     return s;
 }
 

@@ -46,8 +46,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 template <int kAct, bool kGated, bool kStore>
 __global__ void __launch_bounds__(32 * kLanes) dense_dz_kernel(const DenseDzArgs a) {
     __shared__ float red[kLanes][kCols + 4];
-    sm100::chain_next();
     sm100::chain_wait();
+    sm100::chain_next();
     const int c = blockIdx.x * kCols + threadIdx.x * 8;
     const int64_t r0 = (int64_t)blockIdx.y * a.rows_per_block;
     const int64_t r1 = min(r0 + a.rows_per_block, (int64_t)a.T);

@@ -60,7 +60,12 @@ constexpr int kEpiBuf = 32 * 128;       // 32 rows x 128 bytes
 constexpr int kEpiBytes = kEpiWarps * kEpiBuf;
 
 // What a tile's epilogue does.
-enum Mode { kLinear = 0, kGated = 1, kF32 = 2 };
+enum Mode {
+    kLinear,  // bias, activation, residual; bf16, the pre-activations too where wanted
+    kGated,   // the same for two projections and their product
+    kPlain,   // bf16
+    kF32
+};
 
 constexpr int kBHalf = 128;                       // B rows each CTA stages
 constexpr int kMmaN = 2 * kBHalf;
@@ -92,6 +97,7 @@ struct Args {
     bool has_res, has_z0, has_z1;
     float* part;         // partial sums of the split tiles
     uint32_t* counters;  // [split tiles][2 CTAs][8 warps]
+    bool late_wait;      // the kernel before this one writes nothing that this one uses
     int32_t* flags;
 };
 
@@ -228,8 +234,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    if (!a.late_wait) chain_wait();
     chain_next();
-    chain_wait();
     const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
 
     if (warp == 0) {
@@ -444,6 +450,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                                      __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
                     store_buf(ti.prob ? &mD1 : &mD0, buf, lane, col, row);
                 }
+            } else if (kMode == kPlain) {
+#pragma unroll 1
+                for (int j = 0; j < kChunks; ++j) {
+                    float v[64];
+                    tmem_ld64(tq + acc_col(2 * j), v);
+                    if (j == kChunks - 1) accumulator_free();
+                    const int col = col0 + j * kChunk;
+                    if (col >= a.N) continue;
+                    uint32_t o[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = pack2(v[2 * i], v[2 * i + 1]);
+                    buffer_free(lane);
+                    stage16(buf, lane, 0, o);
+                    stage16(buf, lane, 1, o + 16);
+                    store_buf(ti.prob ? &mD1 : &mD0, buf, lane, col, row);
+                }
             } else if (kMode == kGated) {
                 // the kept projections first, one at a time through the buffer
 #pragma unroll 1
@@ -531,12 +553,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                         }
                         stage16(buf, lane, 0, y);
                         stage16(buf, lane, 1, y + 16);
-                        store_buf(ti.prob ? &mD1 : &mD0, buf, lane, col, row);
+                        store_buf(&mD0, buf, lane, col, row);
                     }
                 }
             }
         }
-        if (lane == 0) bulk_wait_all();
+        if (lane == 0) bulk_wait_read<0>();  // the stores land before the kernel counts as complete
     }
 
     __syncwarp();  // the single-lane roles join their warps
@@ -545,6 +567,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
         // any still in flight time to land before shared memory is released
         for (int i = 0; i < 2000; ++i) __nanosleep(100);
     }
+    // what follows this kernel may count on the one before it having completed
+    if (a.late_wait) chain_wait();
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
@@ -646,6 +670,11 @@ double dense_pairs_steps(int64_t T, int N, int64_t k, int segs, bool gated) {
     const Problem p{T, N, gated ? 128 : 256, cdiv(k, kBK), segs, 1};
     return (double)(p.tiles() / kDensePairs) * p.seg_steps * segs + p.plan().cost;
 }
+int dense_dgrad_pairs_ctas(int64_t T, int K, int N, int segs) {
+    const Problem p = dgrad_problem(T, K, N, segs);
+    const TailPlan t = p.plan();
+    return 2 * std::min(kDensePairs, t.full + t.slots * t.splits);
+}
 size_t dense_fwd_pairs_part_floats(int64_t T, int K, int N, bool gated) {
     return fwd_problem(T, K, N, gated).part_floats();
 }
@@ -693,11 +722,11 @@ cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const voi
         ok = ok && make_tile_map(&m.A1, false, dz1, N, T, 1, kBM) && make_tile_map(&m.B1, false, w1, K, N, 1, 64);
     if (!ok) return cudaErrorInvalidValue;
     const Args a = args_of(dgrad_problem(T, K, N, dz1 ? 2 : 1), ws);
-    return launch<kLinear, false, true>(m, a, dz1 ? "gated_dgrad" : "linear_dgrad", st);
+    return launch<kPlain, false, true>(m, a, dz1 ? "gated_dgrad" : "linear_dgrad", st);
 }
 
 cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, int64_t T, int K, int N, void* dw0,
-                               void* dw1, bool f32, const DenseWs& ws, cudaStream_t st) {
+                               void* dw1, bool f32, bool beside, const DenseWs& ws, cudaStream_t st) {
     Maps m;
     bool ok = make_tile_map(&m.A0, false, dz0, N, T, 1, 64) && make_tile_map(&m.B0, false, x, K, T, 1, 64) &&
               make_tile_map(&m.D0, f32, dw0, K, N, 1, 32);
@@ -706,9 +735,10 @@ cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, 
     m.D1 = m.D2 = m.R = m.D0;
     if (dz1) ok = ok && make_tile_map(&m.A1, false, dz1, N, T, 1, 64) && make_tile_map(&m.D1, f32, dw1, K, N, 1, 32);
     if (!ok) return cudaErrorInvalidValue;
-    const Args a = args_of(wgrad_problem(T, K, N, dz1 ? 2 : 1), ws);
+    Args a = args_of(wgrad_problem(T, K, N, dz1 ? 2 : 1), ws);
+    a.late_wait = beside;
     const char* name = dz1 ? "gated_wgrad" : "linear_wgrad";
-    return f32 ? launch<kF32, true, true>(m, a, name, st) : launch<kLinear, true, true>(m, a, name, st);
+    return f32 ? launch<kF32, true, true>(m, a, name, st) : launch<kPlain, true, true>(m, a, name, st);
 }
 
 }  // namespace moe

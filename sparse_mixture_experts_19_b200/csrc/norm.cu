@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1) norm_fwd_kernel(const NormArgs a,
         for (int s = 0; s < geo.S; ++s)
             if (first + s * step < a.T) issue(first + s * step, s);
     }
-    chain_next();
     chain_wait();
+    chain_next();
     g.sync();
     // the thread's columns of w and b stay in registers over all its rows
     float w[kVpt][8], b[kVpt][8];
@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormArgs a,
         for (int s = 0; s < geo.S; ++s)
             if (first + s * step < a.T) issue(first + s * step, s);
     }
-    chain_next();
     chain_wait();
+    chain_next();
     g.sync();
     const float inv = 1.f / (float)a.H;
     float w[kVpt][8], dw[kVpt][8] = {}, db[kVpt][8] = {};
@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormArgs a,
 __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, int64_t stride, int P,
                                                             int64_t second, int N, float* out0, float* out1) {
     __shared__ float s[32][33];
-    chain_next();
     chain_wait();
+    chain_next();
     float* out = blockIdx.y ? out1 : out0;
     if (!out) return;
     const int c = blockIdx.x * 32 + threadIdx.x;

@@ -140,7 +140,9 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 // tensor maps), then calls chain_wait before its first access to global
 // memory: that returns when the kernel before has completed and its writes are
 // visible.  chain_next lets the kernel after it start in the same way, once
-// every CTA of this one has called it.
+// every CTA of this one has called it.  Every kernel calls chain_wait first and
+// chain_next second: a kernel that has started then knows that the one before
+// the one before it has completed.
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -195,8 +197,6 @@ template <int kLeft>
 __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
 }
-// Until every bulk group of this thread is complete.
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Orders this thread's shared-memory accesses before later asynchronous copies.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
