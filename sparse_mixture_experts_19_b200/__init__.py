@@ -448,38 +448,55 @@ class _Call:
     """Argument marshalling of one call: the current device and its stream are
     looked up once, each tensor's type, shape, layout and device checked."""
 
-    __slots__ = ("dev", "f32", "bf16")
+    __slots__ = ("dev",)
 
     def __init__(self):
         import torch
 
-        self.dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
-        self.f32, self.bf16 = torch.float32, torch.bfloat16
+        try:
+            self.dev = torch.cuda.current_device()
+        except (RuntimeError, AssertionError):  # no CUDA device: every tensor is refused below
+            self.dev = -2
 
-    def arg(self, t, name: str, shape: tuple, dtype: int, optional: bool = False):
-        """Device pointer of a contiguous tensor of this shape and MOE_* dtype
-        on the current device (ints pass through as raw pointers)."""
+    def arg(self, t, name: str, shape: tuple, dtype, optional: bool = False):
+        """Device pointer of a contiguous tensor of this shape and dtype on the
+        current device (ints pass through as raw pointers)."""
         if t is None:
             if optional:
                 return None
             raise MoeError(1, f"{name} is None")
         if isinstance(t, int):
             return t
-        want = self.bf16 if dtype == MOE_BF16 else self.f32
-        if t.dtype is not want:
-            raise MoeError(1, f"{name} is {t.dtype}, not {want}")
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self.dev and t.is_contiguous():
+            return t.data_ptr()
+        if t.dtype is not dtype:
+            raise MoeError(1, f"{name} is {t.dtype}, not {dtype}")
         if t.shape != shape:
             raise MoeError(1, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-        p = _ptr(t)
-        if t.get_device() != self.dev:
-            raise MoeError(1, f"{name} is on {t.device}, not on the current device")
-        return p
+        _ptr(t)
+        raise MoeError(1, f"{name} is on {t.device}, not on the current device")
 
     def ws(self, ws):
         """(pointer, bytes) of a workspace on the current device."""
-        if ws is not None and not isinstance(ws, int) and ws.is_cuda and ws.get_device() != self.dev:
+        if ws is None or isinstance(ws, int):
+            return _ws(ws)
+        if ws.is_cuda and ws.get_device() != self.dev:
             raise MoeError(1, f"ws is on {ws.device}, not on the current device")
-        return _ws(ws)
+        return _ptr(ws), ws.nbytes
+
+    def stream(self, stream):
+        if stream is None:
+            import torch
+
+            return torch._C._cuda_getCurrentRawStream(self.dev)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _torch_types():
+    """(torch dtype of each MOE_* dtype, float32)"""
+    import torch
+
+    return (torch.float32, torch.bfloat16), torch.float32
 
 
 def _sized(size_fn, cfg) -> int:
@@ -540,81 +557,81 @@ def gated_backward_workspace(cfg, device="cuda"):
 
 def moe_norm_forward(cfg, x, weight, bias, y, mean_out=None, rstd_out=None, stream=None):
     """y = norm(x); mean_out, rstd_out [T] float32 keep the statistics."""
-    T, H, d = cfg.T, cfg.H, cfg.dtype
-    c = _Call()
-    arg = c.arg
+    T, H = cfg.T, cfg.H
+    c, (types, f32) = _Call(), _torch_types()
+    arg, d = c.arg, types[cfg.dtype]
     _check(load().moe_norm_forward(ctypes.byref(cfg), arg(x, "x", (T, H), d),
-                                   arg(weight, "weight", (H,), MOE_F32, True),
-                                   arg(bias, "bias", (H,), MOE_F32, True), arg(y, "y", (T, H), d),
-                                   arg(mean_out, "mean_out", (T,), MOE_F32, True),
-                                   arg(rstd_out, "rstd_out", (T,), MOE_F32, True), _stream(stream)))
+                                   arg(weight, "weight", (H,), f32, True),
+                                   arg(bias, "bias", (H,), f32, True), arg(y, "y", (T, H), d),
+                                   arg(mean_out, "mean_out", (T,), f32, True),
+                                   arg(rstd_out, "rstd_out", (T,), f32, True), c.stream(stream)))
 
 
 def moe_norm_backward(cfg, dy, x, weight, mean, rstd, d_residual, dx, d_weight, d_bias, ws, stream=None):
     """dx (+ d_residual), d_weight and d_bias (each may be None) of the norm."""
-    T, H, d = cfg.T, cfg.H, cfg.dtype
-    c = _Call()
-    arg = c.arg
+    T, H = cfg.T, cfg.H
+    c, (types, f32) = _Call(), _torch_types()
+    arg, d = c.arg, types[cfg.dtype]
     p, n = c.ws(ws)
-    _check(load().moe_norm_backward(ctypes.byref(cfg), arg(dy, "dy", (T, H), cfg.dy_dtype),
-                                    arg(x, "x", (T, H), d), arg(weight, "weight", (H,), MOE_F32, True),
-                                    arg(mean, "mean", (T,), MOE_F32, True), arg(rstd, "rstd", (T,), MOE_F32),
+    _check(load().moe_norm_backward(ctypes.byref(cfg), arg(dy, "dy", (T, H), types[cfg.dy_dtype]),
+                                    arg(x, "x", (T, H), d), arg(weight, "weight", (H,), f32, True),
+                                    arg(mean, "mean", (T,), f32, True), arg(rstd, "rstd", (T,), f32),
                                     arg(d_residual, "d_residual", (T, H), d, True), arg(dx, "dx", (T, H), d),
-                                    arg(d_weight, "d_weight", (H,), MOE_F32, True),
-                                    arg(d_bias, "d_bias", (H,), MOE_F32, True), p, n, _stream(stream)))
+                                    arg(d_weight, "d_weight", (H,), f32, True),
+                                    arg(d_bias, "d_bias", (H,), f32, True), p, n, c.stream(stream)))
 
 
 def moe_linear_forward(cfg, x, w, bias, residual, y, z_out=None, ws=None, stream=None):
     """y = act(x w^T + bias) + residual; z_out keeps the pre-activations."""
-    T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
-    c = _Call()
-    arg = c.arg
+    T, K, N = cfg.T, cfg.K, cfg.N
+    c, (types, f32) = _Call(), _torch_types()
+    arg, d = c.arg, types[cfg.dtype]
     _check(load().moe_linear_forward(ctypes.byref(cfg), arg(x, "x", (T, K), d), arg(w, "w", (N, K), d),
-                                     arg(bias, "bias", (N,), MOE_F32, True),
+                                     arg(bias, "bias", (N,), f32, True),
                                      arg(residual, "residual", (T, N), d, True), arg(y, "y", (T, N), d),
-                                     arg(z_out, "z_out", (T, N), d, True), *c.ws(ws), _stream(stream)))
+                                     arg(z_out, "z_out", (T, N), d, True), *c.ws(ws), c.stream(stream)))
 
 
 def moe_linear_backward(cfg, dy, x, w, z, dx, d_w, d_bias, ws=None, stream=None):
     """dx, d_w, d_bias (each may be None) of the linear layer."""
-    T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
-    c = _Call()
-    arg = c.arg
+    T, K, N = cfg.T, cfg.K, cfg.N
+    c, (types, f32) = _Call(), _torch_types()
+    arg, d = c.arg, types[cfg.dtype]
     _check(load().moe_linear_backward(ctypes.byref(cfg), arg(dy, "dy", (T, N), d),
                                       arg(x, "x", (T, K), d, d_w is None), arg(w, "w", (N, K), d, dx is None),
                                       arg(z, "z", (T, N), d, True), arg(dx, "dx", (T, K), d, True),
-                                      arg(d_w, "d_w", (N, K), cfg.grad_dtype, True),
-                                      arg(d_bias, "d_bias", (N,), MOE_F32, True), *c.ws(ws), _stream(stream)))
+                                      arg(d_w, "d_w", (N, K), types[cfg.grad_dtype], True),
+                                      arg(d_bias, "d_bias", (N,), f32, True), *c.ws(ws), c.stream(stream)))
 
 
 def moe_gated_forward(cfg, x, w_gate, w_up, b_gate, b_up, h, g_out=None, u_out=None, ws=None, stream=None):
     """h = act(x w_gate^T + b_gate) * (x w_up^T + b_up); g_out, u_out keep the
     two projections."""
-    T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
-    c = _Call()
-    arg = c.arg
+    T, K, N = cfg.T, cfg.K, cfg.N
+    c, (types, f32) = _Call(), _torch_types()
+    arg, d = c.arg, types[cfg.dtype]
     _check(load().moe_gated_forward(ctypes.byref(cfg), arg(x, "x", (T, K), d), arg(w_gate, "w_gate", (N, K), d),
-                                    arg(w_up, "w_up", (N, K), d), arg(b_gate, "b_gate", (N,), MOE_F32, True),
-                                    arg(b_up, "b_up", (N,), MOE_F32, True), arg(h, "h", (T, N), d),
+                                    arg(w_up, "w_up", (N, K), d), arg(b_gate, "b_gate", (N,), f32, True),
+                                    arg(b_up, "b_up", (N,), f32, True), arg(h, "h", (T, N), d),
                                     arg(g_out, "g_out", (T, N), d, True), arg(u_out, "u_out", (T, N), d, True),
-                                    *c.ws(ws), _stream(stream)))
+                                    *c.ws(ws), c.stream(stream)))
 
 
 def moe_gated_backward(cfg, dh, x, w_gate, w_up, g, u, dx, d_w_gate, d_w_up, d_b_gate=None, d_b_up=None, ws=None,
                        stream=None):
     """dx, the two weight gradients and the two bias gradients (each may be
     None) of the gate/up projections."""
-    T, K, N, d = cfg.T, cfg.K, cfg.N, cfg.dtype
-    c = _Call()
-    arg = c.arg
+    T, K, N = cfg.T, cfg.K, cfg.N
+    c, (types, f32) = _Call(), _torch_types()
+    arg, d = c.arg, types[cfg.dtype]
     no_dw = d_w_gate is None and d_w_up is None
     _check(load().moe_gated_backward(
         ctypes.byref(cfg), arg(dh, "dh", (T, N), d), arg(x, "x", (T, K), d, no_dw),
         arg(w_gate, "w_gate", (N, K), d, dx is None), arg(w_up, "w_up", (N, K), d, dx is None),
         arg(g, "g", (T, N), d), arg(u, "u", (T, N), d), arg(dx, "dx", (T, K), d, True),
-        arg(d_w_gate, "d_w_gate", (N, K), cfg.grad_dtype, True), arg(d_w_up, "d_w_up", (N, K), cfg.grad_dtype, True),
-        arg(d_b_gate, "d_b_gate", (N,), MOE_F32, True), arg(d_b_up, "d_b_up", (N,), MOE_F32, True), *c.ws(ws),
-        _stream(stream)))
+        arg(d_w_gate, "d_w_gate", (N, K), types[cfg.grad_dtype], True), arg(d_w_up, "d_w_up", (N, K), types[cfg.grad_dtype], True),
+        arg(d_b_gate, "d_b_gate", (N,), f32, True), arg(d_b_up, "d_b_up", (N,), f32, True), *c.ws(ws),
+        c.stream(stream)))
 
 
 def moe_dense_get_device_status(ws, stream=None) -> int:

@@ -206,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(rbar + kEpiWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // warp: uniform
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
@@ -281,10 +281,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader)
-        // One thread's instruction stream paces the tensor core, so it is kept
-        // short: descriptors by addition, the next step's barrier tested while
-        // this step's MMAs are being issued.
-        if (lane == 0 && leader) {
+        // (the whole warp, one lane elected).  One warp's instruction stream paces
+        // the tensor core, so it is kept short: descriptors by addition, the
+        // next stage's barrier tested while this one's MMAs are being issued.
+        if (leader) {
             constexpr uint32_t kIdesc = idesc_bf16_major(2 * kBM, kMmaN, kAMN, kBMN);
             constexpr uint32_t kStepA = (kAMN ? 2048 : 32) >> 4, kStepB = (kBMN ? 2048 : 32) >> 4;
             const uint32_t base = smem_u32(smem);
@@ -317,15 +317,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                     for (int j = 0; j < n; ++j, da += kStepBytes >> 4, db += kStepBytes >> 4)
 #pragma unroll
                         for (int kk = 0; kk < kBK / 16; ++kk) {
-                            mma_bf16_pair(d, da + kk * kStepA, db + kk * kStepB, kIdesc, sum);
+                            mma_bf16_pair_warp(d, da + kk * kStepA, db + kk * kStepB, kIdesc, sum);
                             sum = 1;
                         }
-                    mma_commit_pair(&empty[cur], 0x3);  // frees the stage in both CTAs
+                    mma_commit_pair_warp(&empty[cur], 0x3);  // frees the stage in both CTAs
                 }
                 if (!ok) break;
-                mma_commit_pair(&tfull[acc], 0x3);
+                mma_commit_pair_warp(&tfull[acc], 0x3);
             }
-            mma_commit_pair(drain, 0x1);
+            mma_commit_pair_warp(drain, 0x1);
             drain_wait(drain, 0);
         }
     } else {

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // warp: uniform
     const uint32_t rank = a.splits > 1 ? cluster_ctarank() : 0;
     const int n0 = (int)(blockIdx.x / a.splits) * 128, t0 = (int)blockIdx.y * a.tn;
     const int ks0 = (int)((int64_t)a.steps * rank / a.splits), ks1 = (int)((int64_t)a.steps * (rank + 1) / a.splits);
@@ -164,34 +164,33 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
             for (int j = std::max(0, it - a.stages); j < it; ++j) drain_wait(&full[j % a.stages], (j / a.stages) & 1);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t idesc = idesc_bf16_major(128, a.tn, kAMN, false);
-            int s = 0;
-            uint32_t ph = 0;
-            for (int ks = ks0; ks < ks1; ++ks) {
-                if (!wait_or_abort(&full[s], ph, abort_flag, a.flags)) break;
-                tc_fence_after();
-                const uint32_t a0 = smem_u32(smem + s * stage_bytes), b0 = a0 + (kGated ? 2 : 1) * kABytes;
+        // ------------------------------------------------ MMA issuer (the whole warp, one lane elected)
+        const uint32_t idesc = idesc_bf16_major(128, a.tn, kAMN, false);
+        const uint32_t base = smem_u32(smem);
+        constexpr uint32_t kStepA = (kAMN ? 2048 : 32) >> 4;
+        const uint64_t da0 = kAMN ? desc_mnmajor_sw128(base, kBox, 1024) : desc_kmajor_sw128(base);
+        const uint64_t db0 = desc_kmajor_sw128(base + (kGated ? 2 : 1) * kABytes);
+        const uint32_t stride = stage_bytes >> 4;
+        int s = 0;
+        uint32_t ph = 0, sum = 0;
+        for (int ks = ks0; ks < ks1; ++ks) {
+            if (!wait_or_abort(&full[s], ph, abort_flag, a.flags)) break;
+            tc_fence_after();
+            const uint64_t da = da0 + (uint32_t)s * stride, db = db0 + (uint32_t)s * stride;
 #pragma unroll
-                for (int kk = 0; kk < kBK / 16; ++kk) {
-                    const uint64_t da =
-                        kAMN ? desc_mnmajor_sw128(a0 + kk * 2048, kBox, 1024) : desc_kmajor_sw128(a0 + kk * 32);
-                    const uint64_t db = desc_kmajor_sw128(b0 + kk * 32);
-                    mma_bf16(tmem_base, da, db, idesc, ks > ks0 || kk > 0);
-                    if (kGated)
-                        mma_bf16(tmem_base + a.tn, desc_kmajor_sw128(a0 + kABytes + kk * 32), db, idesc,
-                                 ks > ks0 || kk > 0);
-                }
-                mma_commit(&empty[s]);
-                if (++s == a.stages) {
-                    s = 0;
-                    ph ^= 1;
-                }
+            for (int kk = 0; kk < kBK / 16; ++kk) {
+                mma_bf16_warp(tmem_base, da + kk * kStepA, db + kk * 2, idesc, sum);
+                if (kGated) mma_bf16_warp(tmem_base + a.tn, da + (kABytes >> 4) + kk * kStepA, db + kk * 2, idesc, sum);
+                sum = 1;
             }
-            mma_commit(done);
-            drain_wait(done, 0);
+            mma_commit_warp(&empty[s]);
+            if (++s == a.stages) {
+                s = 0;
+                ph ^= 1;
+            }
         }
+        mma_commit_warp(done);
+        drain_wait(done, 0);
     } else if (warp < 10) {
         // ------------------------------------------------ TMEM -> part[accumulator][token][128 features]
         // (in the ring's place: the accumulator is complete, so every step's
