@@ -55,7 +55,7 @@ struct DenseDzArgs {
     float* part;             // [dense_dz_row_blocks][1 or 2][N]
 };
 
-int dense_dz_row_blocks(int64_t T, int64_t N);
+int dense_dz_row_blocks(int64_t T, int64_t N, bool gated);
 // dz (dg, du) and, where db0 / db1 are non-null, the bias gradients.
 cudaError_t launch_dense_dz(DenseDzArgs a, bool gated, int act, float* db0, float* db1, cudaStream_t st);
 // ---- tensor-core products (operands bf16, row-major, float32 accumulators)

@@ -75,7 +75,7 @@ void make_dense_plan(const moe_dense_config_t* c, bool gated, bool backward, voi
         const size_t tn = (size_t)c->T * c->N;
         if (gated || c->act != MOE_ACT_NONE) p->dz0 = (bf16*)take(tn * 2);
         if (gated) p->dz1 = (bf16*)take(tn * 2);
-        p->sums = (float*)take(sizeof(float) * two * c->N * dense_dz_row_blocks(c->T, c->N));
+        p->sums = (float*)take(sizeof(float) * two * c->N * dense_dz_row_blocks(c->T, c->N, gated));
         p->ws.part = (float*)take(sizeof(float) * dense_dgrad_part_floats(c->T, c->K, c->N, two));
         p->wws.part = (float*)take(sizeof(float) * dense_wgrad_part_floats(c->T, c->K, c->N, two));
     } else if (c->T > 0) {

@@ -22,6 +22,9 @@ namespace {
 
 constexpr int kCols = 256;  // columns per block: 32 threads x 8
 constexpr int kLanes = 8;   // row lanes per block
+// Blocks of an SM at once: the grid is one wave of them (a second, partial wave
+// cost a third of the time), each walking as many rows as that takes.
+constexpr int kBlocksLinear = 6, kBlocksGated = 4;
 
 __device__ __forceinline__ void unpack8(const uint4& a, float (&v)[8]) {
     const uint32_t u[4] = {a.x, a.y, a.z, a.w};
@@ -44,7 +47,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // kAct: the activation; kGated: dg and du from dh, g, u; kStore: write dz
 // (false: column sums of dy alone, kAct none).
 template <int kAct, bool kGated, bool kStore>
-__global__ void __launch_bounds__(32 * kLanes) dense_dz_kernel(const DenseDzArgs a) {
+__global__ void __launch_bounds__(32 * kLanes, kGated ? kBlocksGated : kBlocksLinear) dense_dz_kernel(const DenseDzArgs a) {
     __shared__ float red[kLanes][kCols + 4];
     sm100::chain_wait();
     sm100::chain_next();
@@ -106,16 +109,15 @@ __global__ void __launch_bounds__(32 * kLanes) dense_dz_kernel(const DenseDzArgs
 
 }  // namespace
 
-// Row ranges: enough blocks to fill the GPU about 8 times over (2048 threads
-// of an SM hold 8 blocks), each of at least 8 rows.
-int dense_dz_row_blocks(int64_t T, int64_t N) {
+// Row ranges: one wave of blocks, each of at least 8 rows.
+int dense_dz_row_blocks(int64_t T, int64_t N, bool gated) {
     const int64_t cb = (N + kCols - 1) / kCols;
-    const int64_t want = std::max<int64_t>(1, (8 * 148 + cb - 1) / cb);
+    const int64_t want = std::max<int64_t>(1, 148 * (gated ? kBlocksGated : kBlocksLinear) / cb);
     return (int)std::min<int64_t>(want, std::max<int64_t>(1, (T + kLanes - 1) / kLanes));
 }
 
 cudaError_t launch_dense_dz(DenseDzArgs a, bool gated, int act, float* db0, float* db1, cudaStream_t st) {
-    const int rb = dense_dz_row_blocks(a.T, a.N);
+    const int rb = dense_dz_row_blocks(a.T, a.N, gated);
     a.rows_per_block = (a.T + rb - 1) / rb;
     const bool store = a.dz != nullptr;
     if (!(db0 || db1)) a.part = nullptr;
