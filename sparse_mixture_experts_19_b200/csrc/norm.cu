@@ -39,7 +39,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRingBytes = 200 * 1024;
 constexpr int kMaxSlots = 8;
-constexpr int kMaxVpt = 4;  // groups of 8 elements per thread (2 where that is enough)
+constexpr int kMaxVpt = 4;  // groups of 8 elements per thread (or 2)
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
@@ -298,8 +298,16 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormArgs a,
     chain_next();
     g.sync();
     const float inv = 1.f / (float)a.H;
-    float w[kVpt][8], dw[kVpt][8] = {}, db[kVpt][8] = {};
-    load_cols(w, a.w, g.t, g.threads, a.H, 1.f);
+    float dw[kVpt][8] = {}, db[kVpt][8] = {};
+    // w stays in registers where there is room, else it is read (from L1) again
+    constexpr bool kHold = kVpt <= 2;
+    float held[kHold ? kVpt : 1][8];
+    if (kHold) load_cols(held, a.w, g.t, g.threads, a.H, 1.f);
+    auto weights = [&](int i, int c, float (&w)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = kHold ? held[kHold ? i : 0][j] : 1.f;
+        if (!kHold && a.w) load8(a.w + c, w);
+    };
     // Row k's two sums, then row k - 1's dx, between two barriers: the second
     // half of the previous row covers the barrier and the warp sums of this one.
     struct Row {
@@ -314,15 +322,16 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormArgs a,
         for (int i = 0; i < kVpt; ++i) {
             const int c = (i * g.threads + g.t) * 8;
             if (c < a.H) {
-                float xh[8], d[8];
+                float xh[8], d[8], w[8];
                 load8(x + c, xh);
                 load8(dy + c, d);
+                weights(i, c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     xh[j] = (xh[j] - o.mu) * r;
                     dw[i][j] = fmaf(d[j], xh[j], dw[i][j]);
                     if (kDb) db[i][j] += d[j];
-                    d[j] *= w[i][j];
+                    d[j] *= w[j];
                     o.s1 += d[j];
                     o.s2 = fmaf(d[j], xh[j], o.s2);
                 }
@@ -341,14 +350,15 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormArgs a,
         for (int i = 0; i < kVpt; ++i) {
             const int c = (i * g.threads + g.t) * 8;
             if (c < a.H) {
-                float xh[8], d[8], v[8] = {};
+                float xh[8], d[8], w[8], v[8] = {};
                 load8(x + c, xh);
                 load8(dy + c, d);
+                weights(i, c, w);
                 if (a.d_res) load8(res + c, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     xh[j] = (xh[j] - o.mu) * o.r;
-                    v[j] += o.r * (fmaf(d[j], w[i][j], -m1) - xh[j] * m2);
+                    v[j] += o.r * (fmaf(d[j], w[j], -m1) - xh[j] * m2);
                 }
                 store8(dx + c, v);
             }
@@ -437,15 +447,15 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, i
     if (threadIdx.y == 0 && c < N) out[c] = s[0][threadIdx.x];
 }
 
-// Warps per row: as few as hold the row in kMaxVpt groups of 8 elements per
-// thread (32 x 32 elements per warp), so that a CTA has several independent
-// rows in flight; more when the slots of a group would otherwise be fewer than
-// three (two rows ahead of the one being worked on).
-Geo geo_of(int H, int slot_bytes) {
+// Warps per row: as few as hold the row in `vpt` groups of 8 elements per
+// thread, so that a CTA has several independent rows in flight; more when the
+// slots of a group would otherwise be fewer than three (two rows ahead of the
+// one being worked on).
+Geo geo_of(int H, int slot_bytes, int vpt) {
     Geo g;
     g.slot_bytes = slot_bytes;
     g.W = 1;
-    while (g.W * 32 * 8 * kMaxVpt < H) g.W *= 2;
+    while (g.W * 32 * 8 * vpt < H) g.W *= 2;
     auto slots = [&] { return std::min(kMaxSlots, kRingBytes / (kWarps / g.W) / slot_bytes); };
     while (g.W < kWarps && slots() < 3) g.W *= 2;
     g.S = std::max(1, slots());
@@ -488,14 +498,17 @@ cudaError_t launch_sum_partials(const float* part, int64_t stride, int P, int64_
 
 template <typename X>
 cudaError_t launch_fwd(const NormArgs& a, cudaStream_t st) {
-    const Geo g = geo_of(a.H, a.H * (int)sizeof(X));
+    const Geo g = geo_of(a.H, a.H * (int)sizeof(X), kMaxVpt);
     return two_vectors(g, a.H) ? launch(norm_fwd_kernel<X, 2>, a, g, "norm_fwd", st)
                                : launch(norm_fwd_kernel<X, kMaxVpt>, a, g, "norm_fwd", st);
 }
 
 template <typename X, typename G, bool kDb>
 cudaError_t launch_bwd(const NormArgs& a, cudaStream_t st) {
-    const Geo g = geo_of(a.H, a.H * (int)(sizeof(X) * (a.d_res ? 2 : 1) + sizeof(G)));
+    // two groups of elements per thread up to H = 8192: with four, the sums of
+    // both weight gradients alone take half of the registers
+    const int vpt = a.H <= kWarps * 32 * 8 * 2 ? 2 : kMaxVpt;
+    const Geo g = geo_of(a.H, a.H * (int)(sizeof(X) * (a.d_res ? 2 : 1) + sizeof(G)), vpt);
     return two_vectors(g, a.H) ? launch(norm_bwd_kernel<X, G, 2, kDb>, a, g, "norm_bwd", st)
                                : launch(norm_bwd_kernel<X, G, kMaxVpt, kDb>, a, g, "norm_bwd", st);
 }
