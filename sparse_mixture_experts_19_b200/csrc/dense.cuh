@@ -82,14 +82,13 @@ size_t dense_fwd_part_floats(int64_t T, int K, int N, bool gated);
 cudaError_t launch_dense_fwd(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
                              const DenseOut& o, const DenseWs& ws, cudaStream_t st);
 // dx [T, K] = dz0 W0 (+ dz1 W1), dz [T, N], W [N, K]; segs = 1 or 2 products.
+// with_wgrad: launch_dense_wgrad of the same dz comes next; *beside tells whether
+// it may then run beside this kernel.
 size_t dense_dgrad_part_floats(int64_t T, int K, int N, int segs);
 cudaError_t launch_dense_dgrad(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T, int K,
-                               int N, void* dx, const DenseWs& ws, cudaStream_t st);
-// Whether that leaves SMs for the weight gradient to run beside it.
-bool dense_dgrad_leaves_room(int64_t T, int K, int N, int segs);
-// dW_p [N, K] = dz_p^T x for one or two dz.  beside: the kernel before it on the
-// stream is launch_dense_dgrad of the same dz with another workspace's partial
-// sums and counters; the two may then run side by side.
+                               int N, void* dx, bool with_wgrad, bool* beside, const DenseWs& ws, cudaStream_t st);
+// dW_p [N, K] = dz_p^T x for one or two dz.  beside: see above; ws has other
+// partial sums and counters than the input gradient's.
 size_t dense_wgrad_part_floats(int64_t T, int K, int N, int problems);
 cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, int64_t T, int K, int N, void* dw0,
                                void* dw1, bool f32, bool beside, const DenseWs& ws, cudaStream_t st);

@@ -670,10 +670,16 @@ double dense_pairs_steps(int64_t T, int N, int64_t k, int segs, bool gated) {
     const Problem p{T, N, gated ? 128 : 256, cdiv(k, kBK), segs, 1};
     return (double)(p.tiles() / kDensePairs) * p.seg_steps * segs + p.plan().cost;
 }
-int dense_dgrad_pairs_ctas(int64_t T, int K, int N, int segs) {
-    const Problem p = dgrad_problem(T, K, N, segs);
+static int ctas_of(const Problem& p) {
     const TailPlan t = p.plan();
     return 2 * std::min(kDensePairs, t.full + t.slots * t.splits);
+}
+int dense_dgrad_pairs_ctas(int64_t T, int K, int N, int segs) { return ctas_of(dgrad_problem(T, K, N, segs)); }
+int dense_wgrad_ctas(int64_t T, int K, int N, int problems) { return ctas_of(wgrad_problem(T, K, N, problems)); }
+double dense_wgrad_us(int64_t T, int K, int N, int problems) {
+    const Problem p = wgrad_problem(T, K, N, problems);
+    const double steps = (double)(p.tiles() / kDensePairs) * p.seg_steps + p.plan().cost;
+    return 6.5 + std::max(0.34 * steps, (double)problems * N * K * 4 / 5.2e6);
 }
 size_t dense_fwd_pairs_part_floats(int64_t T, int K, int N, bool gated) {
     return fwd_problem(T, K, N, gated).part_floats();

@@ -300,24 +300,62 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// The geometry: token tiles of up to 256 tokens (gated: 128, two accumulators),
-// and, where the tiles leave SMs idle, the reduction split over the largest
-// cluster whose clusters all fit on the GPU at once, with at least 4 steps per
-// CTA.
-void fill(Args& a, int64_t T, int N, int64_t k, int segs, bool gated, int32_t* flags) {
-    const int acc = gated ? 2 : 1, most = 256 / acc;
+// One way of laying a product out, and its estimated time in microseconds.
+struct Geometry {
+    int tn, splits;
+    int64_t ctas;
+    double us;
+};
+
+// Token tiles of tn, the reduction split over the largest cluster whose
+// clusters all fit on the GPU at once, with at least 4 steps per CTA.  The
+// estimate is a fit to 220 measured calls (both forward forms, T = 100 ... 800,
+// five weight shapes from 1024 x 1024 to 8192 x 2048, tiles of 64 to 256 tokens;
+// rms error 9%): a step is the slowest of issuing it (0.29 us), its MMAs and its
+// bytes at the rate that the SMs draw from L2 together; then the partial sums
+// that come from peers, and the tile's way out of TMEM and through the epilogue.
+Geometry geometry(int64_t T, int N, int64_t k, int steps, int acc, int tn, int64_t most_ctas) {
+    // clusters of s CTAs with 209 KB of shared memory each that a B200 holds at
+    // once (a cluster stays inside a GPC), a little below what it reports
+    static const int kFit[9] = {0, 148, 74, 44, 32, 26, 20, 0, 14};
+    const int64_t tiles = (int64_t)cdiv(N, 128) * cdiv(T, tn);
+    Geometry g{tn, 1, tiles, 0};
+    for (int s = 2; s <= 8; ++s)
+        if (tiles <= kFit[s] && tiles * s <= most_ctas && steps >= 4 * s) g.splits = s;
+    g.ctas = tiles * g.splits;
+    const double ctas = (double)g.ctas, rounds = (double)cdiv(g.ctas, 148), cols = tn * acc;
+    const double step =
+        std::max({0.29, 0.0016 * cols, (acc * kABytes + tn * kBK * 2) * std::min(ctas, 148.0) / 17.6e6});
+    const double stream = std::max(rounds * cdiv(steps, g.splits) * step, acc * (double)N * k * 2 / 5.2e6);
+    g.us = 2.8 + stream + 0.016 * cols * (g.splits - 1) / g.splits + rounds * cols * (0.0094 + 0.017 / g.splits);
+    return g;
+}
+
+// The best geometry, over token tiles of at most 256 tokens (gated: 128, two
+// accumulators) and down to 32, of at most most_ctas CTAs (tn = 0 when there is
+// none).
+constexpr int64_t kAnyCtas = INT64_MAX;
+Geometry best_geometry(int64_t T, int N, int64_t k, int segs, bool gated, int64_t most_ctas = kAnyCtas) {
+    const int acc = gated ? 2 : 1, steps = cdiv(k, kBK) * segs;
+    const int64_t least = cdiv(T, 256 / acc);
+    Geometry best{};
+    for (int64_t n = least; n < least + 8; ++n) {
+        const int tn = cdiv(cdiv(T, n), 16) * 16;
+        if (n > least && tn < 32) break;
+        const Geometry g = geometry(T, N, k * segs, steps, acc, tn, most_ctas);
+        if (g.ctas <= most_ctas && (best.tn == 0 || g.us < best.us)) best = g;
+    }
+    return best;
+}
+
+void fill(Args& a, const Geometry& g, int64_t T, int N, int64_t k, int segs, bool gated, int32_t* flags) {
+    const int acc = gated ? 2 : 1;
     a.T = (int)T;
     a.N = N;
     a.seg_steps = cdiv(k, kBK);
     a.steps = a.seg_steps * segs;
-    a.tn = cdiv(cdiv(T, cdiv(T, most)), 16) * 16;
-    const int64_t tiles = (int64_t)cdiv(N, 128) * cdiv(T, a.tn);
-    // clusters of s CTAs with 209 KB of shared memory each that a B200 holds at
-    // once (a cluster stays inside a GPC), a little below what it reports
-    static const int kFit[9] = {0, 148, 74, 44, 32, 26, 20, 0, 14};
-    a.splits = 1;
-    for (int s = 2; s <= 8; ++s)
-        if (tiles <= kFit[s] && a.steps >= 4 * s) a.splits = s;
+    a.tn = g.tn;
+    a.splits = g.splits;
     a.stages = std::min(kMaxStages, kRingBytes / (acc * kABytes + a.tn * kBK * 2));
     const uint32_t cols = acc * a.tn;
     a.tmem_cols = 32;
@@ -338,12 +376,10 @@ cudaError_t launch(const CUtensorMap& A0, const CUtensorMap& A1, const CUtensorM
     return e;
 }
 
-}  // namespace
-
-cudaError_t launch_dense_fwd_skinny(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
-                                    const DenseOut& o, int32_t* flags, cudaStream_t st) {
+cudaError_t launch_fwd_skinny(const Geometry& g, const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
+                              const DenseOut& o, int32_t* flags, cudaStream_t st) {
     Args a{};
-    fill(a, T, N, K, 1, w1 != nullptr, flags);
+    fill(a, g, T, N, K, 1, w1 != nullptr, flags);
     a.act = o.act;
     a.bias0 = o.bias0;
     a.bias1 = o.bias1;
@@ -360,10 +396,10 @@ cudaError_t launch_dense_fwd_skinny(const void* x, const void* w0, const void* w
     return launch<false, false>(A0, A1, B, B, a, "linear_fwd_skinny", st);
 }
 
-cudaError_t launch_dense_dgrad_skinny(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T,
-                                      int K, int N, void* dx, int32_t* flags, cudaStream_t st) {
+cudaError_t launch_dgrad_skinny(const Geometry& g, const void* dz0, const void* dz1, const void* w0, const void* w1,
+                                int64_t T, int K, int N, void* dx, int32_t* flags, cudaStream_t st) {
     Args a{};
-    fill(a, T, K, N, dz1 ? 2 : 1, false, flags);
+    fill(a, g, T, K, N, dz1 ? 2 : 1, false, flags);
     a.y = static_cast<bf16*>(dx);
     CUtensorMap A0, A1, B0, B1;
     if (!make_tile_map(&A0, false, w0, K, N, 1, 64) || !make_tile_map(&B0, false, dz0, N, T, 1, a.tn))
@@ -375,60 +411,83 @@ cudaError_t launch_dense_dgrad_skinny(const void* dz0, const void* dz1, const vo
     return launch<false, true>(A0, A1, B0, B1, a, dz1 ? "gated_dgrad_skinny" : "linear_dgrad_skinny", st);
 }
 
-// Which form a product of T rows, N outputs and a reduction of k (in `segs`
-// segments) takes: the one whose estimated time is less.  Both estimates are
-// fits to measurements of both forms at T = 1 ... 1024 on 2880 -> 2880, 4096 ->
-// 14336 and 2048 -> 768 (within 15%), in microseconds:
-//   few rows:  5 + 0.016 per token and accumulator (moving and adding the
-//              partial sums) + the rounds of CTAs x their steps, a step being
-//              the slower of its MMAs and its bytes at the 13 TB/s that the SMs
-//              draw from L2 together;
-//   pairs:     6 + 0.33 per reduction step of the rounds of tiles;
-// and neither reads its operands faster than 6.2 TB/s from HBM.  At T = 128 the
-// few-row form takes 10.0 against 20.4 us on 2880 -> 2880 (pairs: 12 tiles for
-// 74 pairs); at T = 256 it takes 39.7 against 31.6 us on 4096 -> 14336, where
-// 112 feature tiles read the tokens 112 times.
-static bool skinny(int64_t T, int N, int64_t k, int segs, bool gated) {
-    Args a{};
-    fill(a, T, N, k, segs, gated, nullptr);
-    const int acc = gated ? 2 : 1;
-    const double hbm = (acc * segs * (double)N * k + (double)T * k * segs) * 2 / 6.2e6;
-    const int64_t token_tiles = cdiv(T, a.tn), ctas = cdiv(N, 128) * token_tiles * a.splits;
-    const double at_once = (double)std::min<int64_t>(ctas, 148);
-    const double step = std::max(0.0011 * a.tn * acc, (acc * kABytes + a.tn * kBK * 2) * at_once / 13e6);
-    const double few = 5 + 0.016 * a.tn * acc + std::max(hbm, (double)cdiv(ctas, 148) * a.steps / a.splits * step);
-    const double pairs = 6 + std::max(hbm, 0.33 * dense_pairs_steps(T, N, k, segs, gated));
-    return few < pairs;
+// The pair kernel's estimated time for T rows, N outputs and a reduction of k (in
+// `segs` segments): 6.5 us and 0.34 per reduction step of the rounds of tiles,
+// or its operands at 5.2 TB/s.
+double pairs_us(int64_t T, int N, int64_t k, int segs, bool gated) {
+    const double bytes = ((gated ? 2 : 1) * (double)N + (double)T) * k * segs * 2;
+    return 6.5 + std::max(bytes / 5.2e6, 0.34 * dense_pairs_steps(T, N, k, segs, gated));
 }
 
-// The weight gradient runs beside the input gradient where that leaves a third
-// of the SMs idle: 13 instead of 20 us for the gate/up backward pass of 65 x 768
-// -> 2048.  Beside one that fills the GPU it only takes SMs from its last wave
-// (4096 x 4096 -> 14336: 1454 instead of 1354 us).
-bool dense_dgrad_leaves_room(int64_t T, int K, int N, int segs) {
-    if (!skinny(T, K, N, segs, false)) return dense_dgrad_pairs_ctas(T, K, N, segs) <= 98;
-    Args a{};
-    fill(a, T, K, N, segs, false, nullptr);
-    return (int64_t)cdiv(K, 128) * cdiv(T, a.tn) * a.splits <= 98;
+// Which form a product takes: few rows in this geometry, or pairs (few = false).
+struct Choice {
+    bool few;
+    Geometry g;
+    int64_t ctas;
+    double us;
+};
+
+// The form whose estimated time is less.  At T = 128 the few-row form takes 10.0
+// against 20.4 us on 2880 -> 2880 (pairs: 12 tiles for 74 pairs); at T = 256 it
+// takes 39.7 against 31.6 us on 4096 -> 14336, where 112 feature tiles read the
+// tokens 112 times.
+Choice choose(int64_t T, int N, int64_t k, int segs, bool gated, int pair_ctas, int64_t most_ctas = kAnyCtas) {
+    Choice c{false, {}, pair_ctas, pairs_us(T, N, k, segs, gated)};
+    if (T > 65535 * 16) return c;  // the grid's second dimension counts token tiles
+    const Geometry g = best_geometry(T, N, k, segs, gated, most_ctas);
+    if (g.tn && (g.us < c.us || c.ctas > most_ctas)) c = Choice{true, g, g.ctas, g.us};
+    return c;
 }
+
+Choice choose_fwd(int64_t T, int K, int N, bool gated) { return choose(T, N, K, 1, gated, 0); }
+
+// The input gradient's form, and whether the weight gradient (where one follows)
+// runs beside it.  Beside an input gradient that leaves SMs idle it starts at
+// once; so the form is either the fastest by itself, or the fastest that leaves
+// the weight gradient its SMs, whichever ends sooner: 10 instead of 15 us for
+// the backward pass of 512 x 2048 -> 768.  Beside one that fills the GPU it would
+// only take SMs from its last wave (4096 x 4096 -> 14336, gate/up: 1454 instead
+// of 1354 us).
+struct DgradPlan {
+    Choice c;
+    bool beside;
+};
+DgradPlan plan_dgrad(int64_t T, int K, int N, int segs, bool with_wgrad) {
+    const int pair_ctas = dense_dgrad_pairs_ctas(T, K, N, segs);
+    const Choice alone = choose(T, K, N, segs, false, pair_ctas);
+    if (!with_wgrad) return {alone, false};
+    const int64_t room = 148 - dense_wgrad_ctas(T, K, N, segs);
+    const double wgrad = dense_wgrad_us(T, K, N, segs);
+    if (room >= 16) {
+        const Choice fit = choose(T, K, N, segs, false, pair_ctas, room);
+        if (fit.ctas <= room && std::max(fit.us, wgrad) + 1 < alone.us + wgrad) return {fit, true};
+    }
+    return {alone, alone.ctas <= 140};
+}
+
+}  // namespace
 
 size_t dense_fwd_part_floats(int64_t T, int K, int N, bool gated) {
-    return skinny(T, N, K, 1, gated) ? 0 : dense_fwd_pairs_part_floats(T, K, N, gated);
+    return choose_fwd(T, K, N, gated).few ? 0 : dense_fwd_pairs_part_floats(T, K, N, gated);
 }
 size_t dense_dgrad_part_floats(int64_t T, int K, int N, int segs) {
-    return skinny(T, K, N, segs, false) ? 0 : dense_dgrad_pairs_part_floats(T, K, N, segs);
+    const bool pairs = !plan_dgrad(T, K, N, segs, false).c.few || !plan_dgrad(T, K, N, segs, true).c.few;
+    return pairs ? dense_dgrad_pairs_part_floats(T, K, N, segs) : 0;
 }
 
 cudaError_t launch_dense_fwd(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
                              const DenseOut& o, const DenseWs& ws, cudaStream_t st) {
-    return skinny(T, N, K, 1, w1 != nullptr) ? launch_dense_fwd_skinny(x, w0, w1, T, K, N, o, ws.flags, st)
-                     : launch_dense_fwd_pairs(x, w0, w1, T, K, N, o, ws, st);
+    const Choice c = choose_fwd(T, K, N, w1 != nullptr);
+    return c.few ? launch_fwd_skinny(c.g, x, w0, w1, T, K, N, o, ws.flags, st)
+                 : launch_dense_fwd_pairs(x, w0, w1, T, K, N, o, ws, st);
 }
 
 cudaError_t launch_dense_dgrad(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T, int K,
-                               int N, void* dx, const DenseWs& ws, cudaStream_t st) {
-    return skinny(T, K, N, dz1 ? 2 : 1, false) ? launch_dense_dgrad_skinny(dz0, dz1, w0, w1, T, K, N, dx, ws.flags, st)
-                     : launch_dense_dgrad_pairs(dz0, dz1, w0, w1, T, K, N, dx, ws, st);
+                               int N, void* dx, bool with_wgrad, bool* beside, const DenseWs& ws, cudaStream_t st) {
+    const DgradPlan p = plan_dgrad(T, K, N, dz1 ? 2 : 1, with_wgrad);
+    *beside = p.beside;
+    return p.c.few ? launch_dgrad_skinny(p.c.g, dz0, dz1, w0, w1, T, K, N, dx, ws.flags, st)
+                   : launch_dense_dgrad_pairs(dz0, dz1, w0, w1, T, K, N, dx, ws, st);
 }
 
 }  // namespace moe
