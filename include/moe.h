@@ -464,8 +464,9 @@ moe_status_t moe_backward(const moe_config_t* cfg, const void* x, const void* dy
  *   - biases, norm weights and their gradients are float32, as router_b is;
  *   - T = 0 is a valid call: outputs of T rows are empty, weight and bias
  *     gradients are written as zeros;
- *   - every output is written, none accumulated into, and is a fixed
- *     function of the inputs, bit for bit (no atomics);
+ *   - every output is written, none accumulated into, and the same call on
+ *     the same values gives the same bits (no sum depends on timing; which
+ *     outputs a backward call is asked for may choose dx's order of summation);
  *   - a tensor the call writes must not overlap another one of the call,
  *     except where stated;
  *   - NaN and infinity propagate as the formulas have them.

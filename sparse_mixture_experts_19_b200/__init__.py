@@ -492,11 +492,13 @@ class _Call:
         return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _torch_types():
-    """(torch dtype of each MOE_* dtype, float32)"""
+def _torch_type(code: int):
+    """The torch dtype of a MOE_* dtype."""
     import torch
 
-    return (torch.float32, torch.bfloat16), torch.float32
+    if code not in (MOE_F32, MOE_BF16):
+        raise MoeError(1, f"dtype = {code} unknown")
+    return torch.bfloat16 if code == MOE_BF16 else torch.float32
 
 
 def _sized(size_fn, cfg) -> int:
@@ -558,8 +560,8 @@ def gated_backward_workspace(cfg, device="cuda"):
 def moe_norm_forward(cfg, x, weight, bias, y, mean_out=None, rstd_out=None, stream=None):
     """y = norm(x); mean_out, rstd_out [T] float32 keep the statistics."""
     T, H = cfg.T, cfg.H
-    c, (types, f32) = _Call(), _torch_types()
-    arg, d = c.arg, types[cfg.dtype]
+    c, d, f32 = _Call(), _torch_type(cfg.dtype), _torch_type(MOE_F32)
+    arg = c.arg
     _check(load().moe_norm_forward(ctypes.byref(cfg), arg(x, "x", (T, H), d),
                                    arg(weight, "weight", (H,), f32, True),
                                    arg(bias, "bias", (H,), f32, True), arg(y, "y", (T, H), d),
@@ -570,10 +572,10 @@ def moe_norm_forward(cfg, x, weight, bias, y, mean_out=None, rstd_out=None, stre
 def moe_norm_backward(cfg, dy, x, weight, mean, rstd, d_residual, dx, d_weight, d_bias, ws, stream=None):
     """dx (+ d_residual), d_weight and d_bias (each may be None) of the norm."""
     T, H = cfg.T, cfg.H
-    c, (types, f32) = _Call(), _torch_types()
-    arg, d = c.arg, types[cfg.dtype]
+    c, d, f32 = _Call(), _torch_type(cfg.dtype), _torch_type(MOE_F32)
+    arg = c.arg
     p, n = c.ws(ws)
-    _check(load().moe_norm_backward(ctypes.byref(cfg), arg(dy, "dy", (T, H), types[cfg.dy_dtype]),
+    _check(load().moe_norm_backward(ctypes.byref(cfg), arg(dy, "dy", (T, H), _torch_type(cfg.dy_dtype)),
                                     arg(x, "x", (T, H), d), arg(weight, "weight", (H,), f32, True),
                                     arg(mean, "mean", (T,), f32, True), arg(rstd, "rstd", (T,), f32),
                                     arg(d_residual, "d_residual", (T, H), d, True), arg(dx, "dx", (T, H), d),
@@ -584,8 +586,8 @@ def moe_norm_backward(cfg, dy, x, weight, mean, rstd, d_residual, dx, d_weight, 
 def moe_linear_forward(cfg, x, w, bias, residual, y, z_out=None, ws=None, stream=None):
     """y = act(x w^T + bias) + residual; z_out keeps the pre-activations."""
     T, K, N = cfg.T, cfg.K, cfg.N
-    c, (types, f32) = _Call(), _torch_types()
-    arg, d = c.arg, types[cfg.dtype]
+    c, d, f32 = _Call(), _torch_type(cfg.dtype), _torch_type(MOE_F32)
+    arg = c.arg
     _check(load().moe_linear_forward(ctypes.byref(cfg), arg(x, "x", (T, K), d), arg(w, "w", (N, K), d),
                                      arg(bias, "bias", (N,), f32, True),
                                      arg(residual, "residual", (T, N), d, True), arg(y, "y", (T, N), d),
@@ -595,12 +597,12 @@ def moe_linear_forward(cfg, x, w, bias, residual, y, z_out=None, ws=None, stream
 def moe_linear_backward(cfg, dy, x, w, z, dx, d_w, d_bias, ws=None, stream=None):
     """dx, d_w, d_bias (each may be None) of the linear layer."""
     T, K, N = cfg.T, cfg.K, cfg.N
-    c, (types, f32) = _Call(), _torch_types()
-    arg, d = c.arg, types[cfg.dtype]
+    c, d, f32, gt = _Call(), _torch_type(cfg.dtype), _torch_type(MOE_F32), _torch_type(cfg.grad_dtype)
+    arg = c.arg
     _check(load().moe_linear_backward(ctypes.byref(cfg), arg(dy, "dy", (T, N), d),
                                       arg(x, "x", (T, K), d, d_w is None), arg(w, "w", (N, K), d, dx is None),
                                       arg(z, "z", (T, N), d, True), arg(dx, "dx", (T, K), d, True),
-                                      arg(d_w, "d_w", (N, K), types[cfg.grad_dtype], True),
+                                      arg(d_w, "d_w", (N, K), gt, True),
                                       arg(d_bias, "d_bias", (N,), f32, True), *c.ws(ws), c.stream(stream)))
 
 
@@ -608,8 +610,8 @@ def moe_gated_forward(cfg, x, w_gate, w_up, b_gate, b_up, h, g_out=None, u_out=N
     """h = act(x w_gate^T + b_gate) * (x w_up^T + b_up); g_out, u_out keep the
     two projections."""
     T, K, N = cfg.T, cfg.K, cfg.N
-    c, (types, f32) = _Call(), _torch_types()
-    arg, d = c.arg, types[cfg.dtype]
+    c, d, f32 = _Call(), _torch_type(cfg.dtype), _torch_type(MOE_F32)
+    arg = c.arg
     _check(load().moe_gated_forward(ctypes.byref(cfg), arg(x, "x", (T, K), d), arg(w_gate, "w_gate", (N, K), d),
                                     arg(w_up, "w_up", (N, K), d), arg(b_gate, "b_gate", (N,), f32, True),
                                     arg(b_up, "b_up", (N,), f32, True), arg(h, "h", (T, N), d),
@@ -622,14 +624,14 @@ def moe_gated_backward(cfg, dh, x, w_gate, w_up, g, u, dx, d_w_gate, d_w_up, d_b
     """dx, the two weight gradients and the two bias gradients (each may be
     None) of the gate/up projections."""
     T, K, N = cfg.T, cfg.K, cfg.N
-    c, (types, f32) = _Call(), _torch_types()
-    arg, d = c.arg, types[cfg.dtype]
+    c, d, f32, gt = _Call(), _torch_type(cfg.dtype), _torch_type(MOE_F32), _torch_type(cfg.grad_dtype)
+    arg = c.arg
     no_dw = d_w_gate is None and d_w_up is None
     _check(load().moe_gated_backward(
         ctypes.byref(cfg), arg(dh, "dh", (T, N), d), arg(x, "x", (T, K), d, no_dw),
         arg(w_gate, "w_gate", (N, K), d, dx is None), arg(w_up, "w_up", (N, K), d, dx is None),
         arg(g, "g", (T, N), d), arg(u, "u", (T, N), d), arg(dx, "dx", (T, K), d, True),
-        arg(d_w_gate, "d_w_gate", (N, K), types[cfg.grad_dtype], True), arg(d_w_up, "d_w_up", (N, K), types[cfg.grad_dtype], True),
+        arg(d_w_gate, "d_w_gate", (N, K), gt, True), arg(d_w_up, "d_w_up", (N, K), gt, True),
         arg(d_b_gate, "d_b_gate", (N,), f32, True), arg(d_b_up, "d_b_up", (N,), f32, True), *c.ws(ws),
         c.stream(stream)))
 

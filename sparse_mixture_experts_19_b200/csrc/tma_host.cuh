@@ -182,7 +182,8 @@ inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, s
         cfg.numAttrs = 2;
     }
     cfg.attrs = attr;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+    return e == cudaSuccess ? e : cudaGetLastError();  // read, so that it is not left to the next caller
 }
 
 inline int device_sm_count() {

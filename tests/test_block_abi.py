@@ -131,6 +131,8 @@ def test_python_refusals():
         moe.dense_config(1, 8, 8, grad_dtype="f16")
     cfg = moe.dense_config(2, 8, 8)
     x = torch.zeros(2, 8, dtype=torch.bfloat16)
+    with pytest.raises(moe.MoeError, match="unknown"):
+        moe.moe_linear_forward(dense(dtype=7), x, x, None, None, x)
     with pytest.raises(moe.MoeError, match="CUDA"):
         moe.moe_linear_forward(cfg, x, torch.zeros(8, 8, dtype=torch.bfloat16), None, None, x)
     with pytest.raises(moe.MoeError, match="shape"):
