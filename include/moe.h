@@ -466,7 +466,7 @@ moe_status_t moe_backward(const moe_config_t* cfg, const void* x, const void* dy
  *     gradients are written as zeros;
  *   - every output is written, none accumulated into, and the same call on
  *     the same values gives the same bits (no sum depends on timing; which
- *     outputs a backward call is asked for may choose dx's order of summation);
+ *     outputs a backward call is asked for may choose the order of summation);
  *   - a tensor the call writes must not overlap another one of the call,
  *     except where stated;
  *   - NaN and infinity propagate as the formulas have them.

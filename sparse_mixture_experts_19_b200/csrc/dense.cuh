@@ -81,16 +81,22 @@ constexpr size_t kDenseCounterBytes = 4864;  // of one product
 size_t dense_fwd_part_floats(int64_t T, int K, int N, bool gated);
 cudaError_t launch_dense_fwd(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
                              const DenseOut& o, const DenseWs& ws, cudaStream_t st);
+// How a weight gradient runs: its last wave's tiles split over the tokens where
+// that pays; beside: it may start before the launch_dense_dgrad of the same dz
+// just before it on the stream has completed.
+struct WgradPlan {
+    bool split, beside;
+};
 // dx [T, K] = dz0 W0 (+ dz1 W1), dz [T, N], W [N, K]; segs = 1 or 2 products.
-// with_wgrad: launch_dense_wgrad of the same dz comes next; *beside tells whether
-// it may then run beside this kernel.
+// with_wgrad: launch_dense_wgrad of the same dz comes next, with *plan.
 size_t dense_dgrad_part_floats(int64_t T, int K, int N, int segs);
 cudaError_t launch_dense_dgrad(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T, int K,
-                               int N, void* dx, bool with_wgrad, bool* beside, const DenseWs& ws, cudaStream_t st);
-// dW_p [N, K] = dz_p^T x for one or two dz.  beside: see above; ws has other
-// partial sums and counters than the input gradient's.
+                               int N, void* dx, bool with_wgrad, WgradPlan* plan, const DenseWs& ws,
+                               cudaStream_t st);
+// dW_p [N, K] = dz_p^T x for one or two dz.  ws has other partial sums and
+// counters than the input gradient's.
 size_t dense_wgrad_part_floats(int64_t T, int K, int N, int problems);
 cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, int64_t T, int K, int N, void* dw0,
-                               void* dw1, bool f32, bool beside, const DenseWs& ws, cudaStream_t st);
+                               void* dw1, bool f32, WgradPlan plan, const DenseWs& ws, cudaStream_t st);
 
 }  // namespace moe

@@ -259,14 +259,14 @@ moe_status_t moe_linear_backward(const moe_dense_config_t* cfg, const void* dy, 
         a.part = p.sums;
         CUDA_TRY(launch_dense_dz(a, false, cfg->act, d_bias, nullptr, st), "linear_dz");
     }
-    bool beside = false;
+    WgradPlan plan{true, false};
     if (dx)
-        CUDA_TRY(launch_dense_dgrad(dz, nullptr, w, nullptr, cfg->T, cfg->K, cfg->N, dx, d_w != nullptr, &beside, p.ws,
+        CUDA_TRY(launch_dense_dgrad(dz, nullptr, w, nullptr, cfg->T, cfg->K, cfg->N, dx, d_w != nullptr, &plan, p.ws,
                                     st),
                  "linear_dgrad");
     if (d_w)
         CUDA_TRY(launch_dense_wgrad(dz, nullptr, x, cfg->T, cfg->K, cfg->N, d_w, nullptr, cfg->grad_dtype == MOE_F32,
-                                    beside, p.wws, st),
+                                    plan, p.wws, st),
                  "linear_wgrad");
     return MOE_OK;
 }
@@ -344,14 +344,14 @@ moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, c
     a.dz1 = p.dz1;
     a.part = p.sums;
     CUDA_TRY(launch_dense_dz(a, true, cfg->act, d_b_gate, d_b_up, st), "gated_dgu");
-    bool beside = false;
+    WgradPlan plan{true, false};
     if (dx)
         CUDA_TRY(launch_dense_dgrad(p.dz0, p.dz1, w_gate, w_up, cfg->T, cfg->K, cfg->N, dx, d_w_gate != nullptr,
-                                    &beside, p.ws, st),
+                                    &plan, p.ws, st),
                  "gated_dgrad");
     if (d_w_gate)
         CUDA_TRY(launch_dense_wgrad(p.dz0, p.dz1, x, cfg->T, cfg->K, cfg->N, d_w_gate, d_w_up,
-                                    cfg->grad_dtype == MOE_F32, beside, p.wws, st),
+                                    cfg->grad_dtype == MOE_F32, plan, p.wws, st),
                  "gated_wgrad");
     return MOE_OK;
 }

@@ -17,8 +17,8 @@ double dense_pairs_steps(int64_t T, int N, int64_t k, int segs, bool gated);
 // CTAs of the pair kernel's input and weight gradients, and the latter's
 // estimated time.
 int dense_dgrad_pairs_ctas(int64_t T, int K, int N, int segs);
-int dense_wgrad_ctas(int64_t T, int K, int N, int problems);
-double dense_wgrad_us(int64_t T, int K, int N, int problems);
+int dense_wgrad_ctas(int64_t T, int K, int N, int problems, bool split);
+double dense_wgrad_us(int64_t T, int K, int N, int problems, bool split);
 size_t dense_fwd_pairs_part_floats(int64_t T, int K, int N, bool gated);
 size_t dense_dgrad_pairs_part_floats(int64_t T, int K, int N, int segs);
 cudaError_t launch_dense_fwd_pairs(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,

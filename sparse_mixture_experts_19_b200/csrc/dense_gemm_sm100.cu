@@ -24,8 +24,7 @@
 // Tiles that do not fill the last wave of pairs are split along the reduction
 // (tail_plan): every split writes its float32 sums to the workspace, and the
 // one that arrives last at a tile's counter adds them in split order and runs
-// the epilogue.  Nothing waits for another CTA, and the order of the sum is
-// fixed.  The counters count warps' regions (32 rows x half the columns), so no
+// the epilogue (for a weight gradient, a second kernel adds them instead).  Nothing waits for another CTA, and the order of the sum is fixed.  The counters count warps' regions (32 rows x half the columns), so no
 // CTA-wide barrier is needed, and return to zero.
 //
 // Roles (10 warps): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
@@ -96,7 +95,7 @@ struct Args {
     const float* bias1;
     bool has_res, has_z0, has_z1;
     float* part;         // partial sums of the split tiles
-    uint32_t* counters;  // [split tiles][2 CTAs][8 warps]
+    uint32_t* counters;  // [split tiles][2 CTAs][8 warps]; null: sum_units_kernel adds the splits
     bool late_wait;      // the kernel before this one writes nothing that this one uses
     int32_t* flags;
 };
@@ -391,6 +390,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                         __stcg(parts + (int64_t)ti.split * kUnit + (g * 8 + i) * 32,
                                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
                 }
+                if (!a.counters) {
+                    accumulator_free();
+                    continue;
+                }
                 __threadfence();
                 __syncwarp();
                 uint32_t before = 0;
@@ -575,6 +578,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
 }
 
+// The split tiles of a weight gradient, their splits added in order: one thread
+// per 4 columns of a row, a block per 32 columns of a warp's region, so that many
+// splits are added by the whole GPU at once.
+template <typename O>
+__global__ void __launch_bounds__(256) sum_units_kernel(const Args a, O* out0, O* out1) {
+    chain_wait();
+    chain_next();
+    constexpr int kRegion = 4 * 8 * 32, kUnit = 2 * kEpiWarps * kRegion;  // float4
+    const int slot = blockIdx.x, region = blockIdx.y >> 2, g = blockIdx.y & 3;
+    const int i = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const Tile ti = decode<256>(a.full + slot * a.splits, a);
+    const int e = region & 7, warp = e + 2, row = ti.m0 + (region >> 3) * kBM + (warp & 3) * 32 + lane;
+    const int col = ti.n0 + (e >> 2) * 128 + g * 32 + i * 4;
+    if (row >= a.M || col >= a.N) return;
+    const float4* p =
+        reinterpret_cast<const float4*>(a.part) + (int64_t)slot * a.splits * kUnit + region * kRegion + (g * 8 + i) * 32 + lane;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const float4 w = __ldcg(p + (int64_t)s * kUnit);
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    }
+    O* out = (ti.prob ? out1 : out0) + (int64_t)row * a.N + col;
+    if constexpr (sizeof(O) == 4)
+        *reinterpret_cast<float4*>(out) = v;
+    else
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+}
+
 struct Maps {
     CUtensorMap A0, A1, B0, B1, D0, D1, D2, R;
 };
@@ -601,30 +633,30 @@ int band_of(int64_t k) {
 
 // Which tiles are split, and how.  Whole waves of kDensePairs tiles are done
 // whole; the r tiles of the last, partial wave in S units each where that ends
-// sooner: ceil(r S / pairs) rounds of steps / S reduction steps, plus what
-// writing the partial sums and adding S of them costs (L2 round trips of the
-// warps that arrive last).
+// sooner.  Costs in reduction steps (0.32 us): ceil(r S / pairs) rounds of steps
+// / S, and adding the partial sums: by the split that arrives last (its warps wait
+// for L2 round trips), or, for a weight gradient, by a kernel of its own on the
+// whole GPU.  Measured on weight gradients of 6 to 48 tiles and 16 to 512 steps:
+// 6 tiles of 47 steps take 19.3 us whole, 16.8 in 4 splits added in the kernel,
+// 11.0 in 8 added by the second one; a second round of units costs more than it
+// gives.
+enum Split { kWhole, kInKernel, kOwnKernel };
 struct TailPlan {
     int full, splits, slots;
     int cost;  // of the last wave, in steps
 };
-constexpr int kSplitCost = 24, kSplitCostEach = 4;  // in steps of 64
-constexpr int kMaxSplits = 8;
 constexpr int kMaxSplitRounds = 3;  // bounds the workspace: 3 x 74 units of 256 KB
-TailPlan tail_plan(int64_t tiles, int steps) {
+TailPlan tail_plan(int64_t tiles, int steps, Split how) {
     const int r = (int)(tiles % kDensePairs);
-    int best = 1, best_cost = steps;
-    for (int s = 2; s <= kMaxSplits && steps >= 4 * s; ++s) {
+    TailPlan best{(int)tiles, 1, 0, r ? steps : 0};
+    for (int s = 2; how != kWhole && r && s <= (how == kOwnKernel ? 32 : 8) && steps >= 4 * s; ++s) {
         const int rounds = cdiv((int64_t)r * s, kDensePairs);
-        const int cost = rounds * (cdiv(steps, s) + kSplitCost + kSplitCostEach * s);
-        if (rounds <= kMaxSplitRounds && cost < best_cost) {
-            best = s;
-            best_cost = cost;
-        }
+        if (rounds > kMaxSplitRounds) break;
+        const int cost = rounds * cdiv(steps, s) + (rounds - 1) * 25 +
+                         (how == kOwnKernel ? 8 + r * s * 2 / 11 : 12 + 4 * s + r * s / 10);
+        if (cost < best.cost) best = {(int)tiles - r, s, r, cost};
     }
-    if (r == 0) return {(int)tiles, 1, 0, 0};
-    if (best == 1) return {(int)tiles, 1, 0, steps};
-    return {(int)tiles - r, best, r, best_cost};
+    return best;
 }
 
 constexpr int64_t kUnitFloats = 256 * 256;
@@ -634,16 +666,19 @@ static_assert(kCounterBytes <= kDenseCounterBytes, "counters");
 struct Problem {  // M x N outputs over `steps` reduction steps, `problems` times
     int64_t M;
     int N, bn, seg_steps, segs, problems;
+    Split split;
     int64_t tiles() const { return (int64_t)cdiv(M, 2 * kBM) * cdiv(N, bn) * problems; }
-    TailPlan plan() const { return tail_plan(tiles(), seg_steps * segs); }
+    TailPlan plan() const { return tail_plan(tiles(), seg_steps * segs, split); }
     size_t part_floats() const {
         const TailPlan p = plan();
         return (size_t)p.slots * p.splits * kUnitFloats;
     }
 };
-Problem fwd_problem(int64_t T, int K, int N, bool gated) { return {T, N, gated ? 128 : 256, cdiv(K, kBK), 1, 1}; }
-Problem dgrad_problem(int64_t T, int K, int N, int segs) { return {T, K, 256, cdiv(N, kBK), segs, 1}; }
-Problem wgrad_problem(int64_t T, int K, int N, int problems) { return {N, K, 256, cdiv(T, kBK), 1, problems}; }
+Problem fwd_problem(int64_t T, int K, int N, bool gated) { return {T, N, gated ? 128 : 256, cdiv(K, kBK), 1, 1, kInKernel}; }
+Problem dgrad_problem(int64_t T, int K, int N, int segs) { return {T, K, 256, cdiv(N, kBK), segs, 1, kInKernel}; }
+Problem wgrad_problem(int64_t T, int K, int N, int problems, bool split) {
+    return {N, K, 256, cdiv(T, kBK), 1, problems, split ? kOwnKernel : kWhole};
+}
 
 Args args_of(const Problem& pr, const DenseWs& ws) {
     const TailPlan p = pr.plan();
@@ -659,7 +694,7 @@ Args args_of(const Problem& pr, const DenseWs& ws) {
     a.splits = p.splits;
     a.total = p.full + p.slots * p.splits;
     a.part = ws.part;
-    a.counters = ws.counters;
+    a.counters = pr.split == kOwnKernel ? nullptr : ws.counters;
     a.flags = ws.flags;
     return a;
 }
@@ -667,7 +702,7 @@ Args args_of(const Problem& pr, const DenseWs& ws) {
 }  // namespace
 
 double dense_pairs_steps(int64_t T, int N, int64_t k, int segs, bool gated) {
-    const Problem p{T, N, gated ? 128 : 256, cdiv(k, kBK), segs, 1};
+    const Problem p{T, N, gated ? 128 : 256, cdiv(k, kBK), segs, 1, kInKernel};
     return (double)(p.tiles() / kDensePairs) * p.seg_steps * segs + p.plan().cost;
 }
 static int ctas_of(const Problem& p) {
@@ -675,11 +710,13 @@ static int ctas_of(const Problem& p) {
     return 2 * std::min(kDensePairs, t.full + t.slots * t.splits);
 }
 int dense_dgrad_pairs_ctas(int64_t T, int K, int N, int segs) { return ctas_of(dgrad_problem(T, K, N, segs)); }
-int dense_wgrad_ctas(int64_t T, int K, int N, int problems) { return ctas_of(wgrad_problem(T, K, N, problems)); }
-double dense_wgrad_us(int64_t T, int K, int N, int problems) {
-    const Problem p = wgrad_problem(T, K, N, problems);
+int dense_wgrad_ctas(int64_t T, int K, int N, int problems, bool split) {
+    return ctas_of(wgrad_problem(T, K, N, problems, split));
+}
+double dense_wgrad_us(int64_t T, int K, int N, int problems, bool split) {
+    const Problem p = wgrad_problem(T, K, N, problems, split);
     const double steps = (double)(p.tiles() / kDensePairs) * p.seg_steps + p.plan().cost;
-    return 6.5 + std::max(0.34 * steps, (double)problems * N * K * 4 / 5.2e6);
+    return 4.5 + std::max(0.33 * steps, (double)problems * N * K * 4 / 5.2e6);
 }
 size_t dense_fwd_pairs_part_floats(int64_t T, int K, int N, bool gated) {
     return fwd_problem(T, K, N, gated).part_floats();
@@ -688,7 +725,7 @@ size_t dense_dgrad_pairs_part_floats(int64_t T, int K, int N, int segs) {
     return dgrad_problem(T, K, N, segs).part_floats();
 }
 size_t dense_wgrad_part_floats(int64_t T, int K, int N, int problems) {
-    return wgrad_problem(T, K, N, problems).part_floats();
+    return wgrad_problem(T, K, N, problems, true).part_floats();
 }
 
 cudaError_t launch_dense_fwd_pairs(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
@@ -732,7 +769,7 @@ cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const voi
 }
 
 cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, int64_t T, int K, int N, void* dw0,
-                               void* dw1, bool f32, bool beside, const DenseWs& ws, cudaStream_t st) {
+                               void* dw1, bool f32, WgradPlan plan, const DenseWs& ws, cudaStream_t st) {
     Maps m;
     bool ok = make_tile_map(&m.A0, false, dz0, N, T, 1, 64) && make_tile_map(&m.B0, false, x, K, T, 1, 64) &&
               make_tile_map(&m.D0, f32, dw0, K, N, 1, 32);
@@ -741,10 +778,18 @@ cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, 
     m.D1 = m.D2 = m.R = m.D0;
     if (dz1) ok = ok && make_tile_map(&m.A1, false, dz1, N, T, 1, 64) && make_tile_map(&m.D1, f32, dw1, K, N, 1, 32);
     if (!ok) return cudaErrorInvalidValue;
-    Args a = args_of(wgrad_problem(T, K, N, dz1 ? 2 : 1), ws);
-    a.late_wait = beside;
+    Args a = args_of(wgrad_problem(T, K, N, dz1 ? 2 : 1, plan.split), ws);
+    a.late_wait = plan.beside;
     const char* name = dz1 ? "gated_wgrad" : "linear_wgrad";
-    return f32 ? launch<kF32, true, true>(m, a, name, st) : launch<kPlain, true, true>(m, a, name, st);
+    const cudaError_t e = f32 ? launch<kF32, true, true>(m, a, name, st) : launch<kPlain, true, true>(m, a, name, st);
+    if (e != cudaSuccess || a.total == a.full || a.counters) return e;
+    const dim3 grid((a.total - a.full) / a.splits, 2 * kEpiWarps * 4);
+    trace_before("wgrad_sum", st);
+    const cudaError_t e2 =
+        f32 ? launch_chained(sum_units_kernel<float>, grid, 256, 0, 0, st, a, (float*)dw0, (float*)dw1)
+            : launch_chained(sum_units_kernel<bf16>, grid, 256, 0, 0, st, a, (bf16*)dw0, (bf16*)dw1);
+    trace_after(st);
+    return e2;
 }
 
 }  // namespace moe

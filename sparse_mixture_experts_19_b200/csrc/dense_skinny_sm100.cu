@@ -441,28 +441,34 @@ Choice choose(int64_t T, int N, int64_t k, int segs, bool gated, int pair_ctas, 
 
 Choice choose_fwd(int64_t T, int K, int N, bool gated) { return choose(T, N, K, 1, gated, 0); }
 
-// The input gradient's form, and whether the weight gradient (where one follows)
-// runs beside it.  Beside an input gradient that leaves SMs idle it starts at
-// once; so the form is either the fastest by itself, or the fastest that leaves
-// the weight gradient its SMs, whichever ends sooner: 10 instead of 15 us for
-// the backward pass of 512 x 2048 -> 768.  Beside one that fills the GPU it would
-// only take SMs from its last wave (4096 x 4096 -> 14336, gate/up: 1454 instead
-// of 1354 us).
+// The input gradient's form, and how the weight gradient (where one follows)
+// runs.  Beside an input gradient that leaves SMs idle the weight gradient starts
+// at once; so either each runs in its fastest form, one after the other, or the
+// input gradient in the fastest form that leaves the weight gradient (whole or
+// split) its SMs, whichever ends sooner: 10 instead of 15 us for the backward pass
+// of 512 x 2048 -> 768.  Beside one that fills the GPU it would only take SMs from
+// its last wave (4096 x 4096 -> 14336, gate/up: 1454 instead of 1354 us).
 struct DgradPlan {
     Choice c;
-    bool beside;
+    WgradPlan w;
 };
 DgradPlan plan_dgrad(int64_t T, int K, int N, int segs, bool with_wgrad) {
     const int pair_ctas = dense_dgrad_pairs_ctas(T, K, N, segs);
     const Choice alone = choose(T, K, N, segs, false, pair_ctas);
-    if (!with_wgrad) return {alone, false};
-    const int64_t room = 148 - dense_wgrad_ctas(T, K, N, segs);
-    const double wgrad = dense_wgrad_us(T, K, N, segs);
-    if (room >= 16) {
+    DgradPlan best{alone, {true, with_wgrad && alone.ctas <= 140}};
+    if (!with_wgrad) return best;
+    double best_us = alone.us + dense_wgrad_us(T, K, N, segs, true);
+    for (int split = 0; split < 2; ++split) {
+        const int64_t room = 148 - dense_wgrad_ctas(T, K, N, segs, split);
+        if (room < 16) continue;
         const Choice fit = choose(T, K, N, segs, false, pair_ctas, room);
-        if (fit.ctas <= room && std::max(fit.us, wgrad) + 1 < alone.us + wgrad) return {fit, true};
+        const double us = std::max(fit.us, dense_wgrad_us(T, K, N, segs, split)) + 1;
+        if (fit.ctas <= room && us < best_us) {
+            best = {fit, {split != 0, true}};
+            best_us = us;
+        }
     }
-    return {alone, alone.ctas <= 140};
+    return best;
 }
 
 }  // namespace
@@ -483,9 +489,10 @@ cudaError_t launch_dense_fwd(const void* x, const void* w0, const void* w1, int6
 }
 
 cudaError_t launch_dense_dgrad(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T, int K,
-                               int N, void* dx, bool with_wgrad, bool* beside, const DenseWs& ws, cudaStream_t st) {
+                               int N, void* dx, bool with_wgrad, WgradPlan* plan, const DenseWs& ws,
+                               cudaStream_t st) {
     const DgradPlan p = plan_dgrad(T, K, N, dz1 ? 2 : 1, with_wgrad);
-    *beside = p.beside;
+    *plan = p.w;
     return p.c.few ? launch_dgrad_skinny(p.c.g, dz0, dz1, w0, w1, T, K, N, dx, ws.flags, st)
                    : launch_dense_dgrad_pairs(dz0, dz1, w0, w1, T, K, N, dx, ws, st);
 }
