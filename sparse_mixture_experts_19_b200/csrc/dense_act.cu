@@ -14,7 +14,7 @@
 
 #include "act.cuh"
 #include "dense.cuh"
-#include "sm100.cuh"
+#include "sm100_dense.cuh"
 #include "tma_host.cuh"
 
 namespace moe {

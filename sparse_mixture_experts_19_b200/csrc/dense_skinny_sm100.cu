@@ -31,7 +31,7 @@
 #include "act.cuh"
 #include "dense.cuh"
 #include "dense_gemm.cuh"
-#include "sm100.cuh"
+#include "sm100_dense.cuh"
 #include "tma_host.cuh"
 
 namespace moe {

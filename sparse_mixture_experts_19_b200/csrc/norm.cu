@@ -27,7 +27,7 @@
 
 #include "common.cuh"
 #include "dense.cuh"
-#include "sm100.cuh"
+#include "sm100_dense.cuh"
 #include "tma_host.cuh"
 
 namespace moe {
