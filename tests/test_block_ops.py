@@ -227,7 +227,8 @@ def test_linear_forward(gpu_lib, T, K, N, act):
 
 LIN_BWD = [(1, 64, 8, "silu"), (1, 264, 4096, "none"), (7, 136, 72, "gelu"), (64, 520, 264, "relu"),
            (65, 72, 200, "gelu_tanh"), (257, 264, 136, "none"), (300, 2040, 72, "silu"), (72, 2040, 2200, "none"),
-           (2100, 264, 328, "gelu"), (5000, 72, 136, "none"), (1031, 520, 8, "silu"), (2200, 2040, 72, "none")]
+           (2100, 264, 328, "gelu"), (5000, 72, 136, "none"), (1031, 520, 8, "silu"), (2200, 2040, 72, "none"),
+           (4000, 1288, 328, "silu")]
 
 
 @pytest.mark.parametrize("grad", ["f32", "bf16"])
