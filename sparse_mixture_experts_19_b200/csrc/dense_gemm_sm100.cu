@@ -656,6 +656,10 @@ TailPlan tail_plan(int64_t tiles, int steps, Split how) {
                          (how == kOwnKernel ? 8 + r * s * 2 / 11 : 12 + 4 * s + r * s / 10);
         if (cost < best.cost) best = {(int)tiles - r, s, r, cost};
     }
+    // less than a twentieth of the whole is not worth it: with pairs idle in the
+    // last wave the others' clock is higher
+    if (best.splits > 1 && (steps - best.cost) * 20 < (tiles / kDensePairs + 1) * steps)
+        best = {(int)tiles, 1, 0, steps};
     return best;
 }
 
