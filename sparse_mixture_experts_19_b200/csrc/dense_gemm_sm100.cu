@@ -11,27 +11,32 @@
 //   weight gradient dW = dz^T x (two problems for the gated pair): both MN-major
 //
 // One persistent kernel template on CTA pairs (cta_group::2): a tile is 256
-// rows x 256 columns (gated: 128 output columns, 256 accumulator columns), each CTA of the pair stages its own 128 rows of A and
-// half of B, and the leader issues M = 256 MMAs that read both CTAs' shared
-// memory: per CTA and 64-deep reduction step 32 KB arrive for 2 x 128 x 256 x
-// 64 flops, which keeps operand traffic below the tensor pipe's time.  A stage
-// of the ring holds two steps: each wait for a stage and each commit holds up
-// the issuing thread's MMAs by about 120 ns, and with one step per stage they
-// were a fifth of the time.  TMEM holds two accumulators, so a tile's epilogue
-// overlaps the next tile's main loop.  Bound by the tensor pipe at large sizes, by the stores (weight
-// gradients of few tokens) or the operands' HBM reads otherwise.
+// rows x 256 columns (gated: 128 output columns, 256 accumulator columns), each
+// CTA of the pair stages its own 128 rows of A and half of B, and the leader
+// issues M = 256 MMAs that read both CTAs' shared memory: per CTA and 64-deep
+// reduction step 32 KB arrive for 2 x 128 x 256 x 64 flops, which keeps operand
+// traffic below the tensor pipe's time.  A stage of the ring holds two steps:
+// each wait for a stage and each commit holds up the issuing warp's MMAs by
+// about 120 ns, and with one step per stage they were a fifth of the time.  TMEM
+// holds two accumulators, so a tile's epilogue overlaps the next tile's main
+// loop.  Bound by the tensor pipe and the power limit at large sizes (gate/up
+// forward, 4096 x 4096 -> 14336: 618 us in a short run, 1.56 PFLOP/s, the pipe 93%
+// active at 1.46 GHz), by the stores (weight gradients of few tokens) or the
+// operands' HBM reads otherwise.
 //
 // Tiles that do not fill the last wave of pairs are split along the reduction
-// (tail_plan): every split writes its float32 sums to the workspace, and the
-// one that arrives last at a tile's counter adds them in split order and runs
-// the epilogue (for a weight gradient, a second kernel adds them instead).  Nothing waits for another CTA, and the order of the sum is fixed.  The counters count warps' regions (32 rows x half the columns), so no
-// CTA-wide barrier is needed, and return to zero.
+// (tail_plan): every split writes its float32 sums to the workspace, and the one
+// that arrives last at a tile's counter adds them in split order and runs the
+// epilogue (for a weight gradient, a second kernel adds them instead).  Nothing
+// waits for another CTA, and the order of the sum is fixed.  The counters count
+// warps' regions (32 rows x half the columns), so no CTA-wide barrier is needed,
+// and return to zero.
 //
 // Roles (10 warps): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
 // epilogue: warp w drains TMEM lanes 32 (w % 4) and one half of the columns.
 // An epilogue warp stages 32 rows x 128 bytes in shared memory (128-byte
 // swizzle) and stores it by TMA, which clips the ragged edges; the residual
-// tile arrives by TMA in the same buffers before the accumulator is ready.
+// arrives by TMA in the same buffer, the first chunk ahead of the accumulator.
 // Every wait is bounded; a timeout sets MOE_DEVFLAG_WAIT_TIMEOUT and the CTA
 // unwinds.  No multicast loads.
 #include <algorithm>
@@ -281,8 +286,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader)
         // (the whole warp, one lane elected).  One warp's instruction stream paces
-        // the tensor core, so it is kept short: descriptors by addition, the
-        // next stage's barrier tested while this one's MMAs are being issued.
+        // the tensor core, so it is kept short: descriptors by addition, no
+        // division.  (Testing the next stage's barrier ahead gains nothing.)
         if (leader) {
             constexpr uint32_t kIdesc = idesc_bf16_major(2 * kBM, kMmaN, kAMN, kBMN);
             constexpr uint32_t kStepA = (kAMN ? 2048 : 32) >> 4, kStepB = (kBMN ? 2048 : 32) >> 4;
@@ -290,18 +295,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
             const uint64_t da0 = kAMN ? desc_mnmajor_sw128(base, kBox, 1024) : desc_kmajor_sw128(base);
             const uint64_t db0 = kBMN ? desc_mnmajor_sw128(base + kABytes, kBox, 1024) : desc_kmajor_sw128(base + kABytes);
             uint32_t s = 0, ph = 0, tc = 0;
-            bool ready = false;
-            for (int t = pair; t < a.total && !*abort_flag; t += npairs, ++tc) {
+            for (int t = pair; t < a.total && !aborted_warp(abort_flag); t += npairs, ++tc) {
                 const Tile ti = decode<kBN>(t, a);
                 const uint32_t acc = tc & 1;
-                if (!wait_or_abort(&tempty[acc], ((tc >> 1) & 1) ^ 1, abort_flag, a.flags)) break;
+                if (!wait_or_abort_warp(&tempty[acc], ((tc >> 1) & 1) ^ 1, abort_flag, a.flags)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * kAccCols;
                 bool ok = true;
                 uint32_t sum = 0;
                 for (int ks = ti.k0, n; ks < ti.k1; ks += n) {
                     n = stage_steps(ks, ti, a);
-                    if (!ready && !wait_or_abort(&full[s], ph, abort_flag, a.flags)) {
+                    if (!wait_or_abort_warp(&full[s], ph, abort_flag, a.flags)) {
                         ok = false;
                         break;
                     }
@@ -311,7 +315,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                         s = 0;
                         ph ^= 1;
                     }
-                    ready = mbar_test(&full[s], ph);
                     uint64_t da = da0 + cur * (kStageBytes >> 4), db = db0 + cur * (kStageBytes >> 4);
                     for (int j = 0; j < n; ++j, da += kStepBytes >> 4, db += kStepBytes >> 4)
 #pragma unroll
@@ -355,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
             const bool res = kMode == kLinear && a.has_res;
             const bool ahead = res && in && whole;
             if (ahead) fetch_res(0);  // ahead of the accumulator
-            if (!wait_sleep_or_abort(&tfull[acc], (tc >> 1) & 1, abort_flag, a.flags)) {
+            if (!wait_sleep_or_abort_warp(&tfull[acc], (tc >> 1) & 1, abort_flag, a.flags)) {
                 if (ahead) drain_wait(&rbar[e], rph);
                 break;
             }
@@ -514,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                             buffer_free(lane);
                         } else {
                             if (j > 0) fetch_res(j);
-                            if (!wait_or_abort(&rbar[e], rph, abort_flag, a.flags)) drain_wait(&rbar[e], rph);
+                            if (!wait_or_abort_warp(&rbar[e], rph, abort_flag, a.flags)) drain_wait(&rbar[e], rph);
                             rph ^= 1;
                         }
                     }

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
         int s = 0;
         uint32_t ph = 0, sum = 0;
         for (int ks = ks0; ks < ks1; ++ks) {
-            if (!wait_or_abort(&full[s], ph, abort_flag, a.flags)) break;
+            if (!wait_or_abort_warp(&full[s], ph, abort_flag, a.flags)) break;
             tc_fence_after();
             const uint64_t da = da0 + (uint32_t)s * stride, db = db0 + (uint32_t)s * stride;
 #pragma unroll

@@ -8,17 +8,20 @@
 namespace moe {
 namespace sm100 {
 
-// Whether the phase of `parity` has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
+// The waits of sm100.cuh for a whole, converged warp that goes on as one: every
+// lane gets the same answer, also when a time-out or another role's abort
+// reaches only some of them (a warp that split there would never meet again at
+// its next collective instruction).
+__device__ __forceinline__ bool wait_or_abort_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                   int32_t* flags) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, flags));
+}
+__device__ __forceinline__ bool wait_sleep_or_abort_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                         int32_t* flags) {
+    return __all_sync(0xffffffffu, wait_sleep_or_abort(bar, parity, abort_flag, flags));
+}
+__device__ __forceinline__ bool aborted_warp(volatile int* abort_flag) {
+    return __any_sync(0xffffffffu, *abort_flag != 0);
 }
 
 // ------------------------------------------------- programmatic launches
