@@ -11,9 +11,10 @@ namespace moe {
 // the sizes alone.
 constexpr int kDensePairs = 74;
 
-// Reduction steps (64 deep) of the rounds that the pair kernel's busiest pair
-// runs, a split's overhead among them.
-double dense_pairs_steps(int64_t T, int N, int64_t k, int segs, bool gated);
+// Reduction steps (64 deep, 256 columns) of the rounds that the pair kernel's
+// busiest pair runs, a split's overhead among them.
+double dense_fwd_pairs_steps(int64_t T, int K, int N, bool gated);
+double dense_dgrad_pairs_steps(int64_t T, int K, int N, int segs);
 // CTAs of the pair kernel's input and weight gradients, and the latter's
 // estimated time.
 int dense_dgrad_pairs_ctas(int64_t T, int K, int N, int segs);

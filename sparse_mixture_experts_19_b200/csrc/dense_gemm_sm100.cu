@@ -11,10 +11,10 @@
 //   weight gradient dW = dz^T x (two problems for the gated pair): both MN-major
 //
 // One persistent kernel template on CTA pairs (cta_group::2): a tile is 256
-// rows x 256 columns (gated: 128 output columns, 256 accumulator columns), each
-// CTA of the pair stages its own 128 rows of A and half of B, and the leader
-// issues M = 256 MMAs that read both CTAs' shared memory: per CTA and 64-deep
-// reduction step 32 KB arrive for 2 x 128 x 256 x 64 flops, which keeps operand
+// rows x 256 columns (gated: 128 output columns, 256 accumulator columns; the
+// linear forward has 128-column tiles too), each CTA of the pair stages its own
+// 128 rows of A and half of B, and the leader issues M = 256 MMAs that read both
+// CTAs' shared memory: per CTA and 64-deep reduction step 32 KB arrive for 2 x 128 x 256 x 64 flops, which keeps operand
 // traffic below the tensor pipe's time.  A stage of the ring holds two steps:
 // each wait for a stage and each commit holds up the issuing warp's MMAs by
 // about 120 ns, and with one step per stage they were a fifth of the time.  TMEM
@@ -71,20 +71,20 @@ enum Mode {
     kF32
 };
 
-constexpr int kBHalf = 128;                       // B rows each CTA stages
-constexpr int kMmaN = 2 * kBHalf;
-constexpr int kBBytes = kBHalf * kBK * 2;
-constexpr int kStepBytes = kABytes + kBBytes;     // one 64-deep step
-constexpr int kStageBytes = 2 * kStepBytes;       // a stage holds two
-constexpr int kStages = 3;
-constexpr size_t kEpiOff = (size_t)kStages * kStageBytes;
-constexpr size_t kBarOff = kEpiOff + kEpiBytes;
-constexpr size_t kSmem = kBarOff + 512 + 1024;
-static_assert(kSmem <= 227 * 1024, "shared memory");
-
-// Output columns of a tile.
-template <int kMode>
-constexpr int tile_cols() { return kMode == kGated ? 128 : 256; }
+// Tile shape and shared memory of one variant: kBN output columns.
+template <int kMode, int kBN>
+struct Cfg {
+    static constexpr int kBHalf = kMode == kGated ? 128 : kBN / 2;  // B columns each CTA stages
+    static constexpr int kMmaN = 2 * kBHalf;
+    static constexpr int kBBytes = kBHalf * kBK * 2;
+    static constexpr int kStepBytes = kABytes + kBBytes;  // one 64-deep step
+    static constexpr int kStageBytes = 2 * kStepBytes;    // a stage holds two
+    static constexpr int kStages = kBHalf == 128 ? 3 : 4;
+    static constexpr size_t kEpiOff = (size_t)kStages * kStageBytes;
+    static constexpr size_t kBarOff = kEpiOff + kEpiBytes;
+    static constexpr size_t kSmem = kBarOff + 512 + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
 
 struct Args {
     int M, N;        // output rows and columns of one problem
@@ -192,18 +192,18 @@ __device__ __forceinline__ void buffer_free(int lane) {
     __syncwarp();
 }
 
-template <int kMode, bool kAMN, bool kBMN>
+template <int kMode, bool kAMN, bool kBMN, int kBN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_gemm_kernel(
     const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mA1,
     const __grid_constant__ CUtensorMap mB0, const __grid_constant__ CUtensorMap mB1,
     const __grid_constant__ CUtensorMap mD0, const __grid_constant__ CUtensorMap mD1,
     const __grid_constant__ CUtensorMap mD2, const __grid_constant__ CUtensorMap mR, const Args a) {
-    constexpr int kBN = tile_cols<kMode>();
+    using C = Cfg<kMode, kBN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);  // used in the leader
-    uint64_t* empty = full + kStages;
-    uint64_t* tfull = empty + kStages;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // used in the leader
+    uint64_t* empty = full + C::kStages;
+    uint64_t* tfull = empty + C::kStages;
     uint64_t* tempty = tfull + 2;  // used in the leader: 8 epilogue warps x 2 CTAs
     uint64_t* drain = tempty + 2;
     uint64_t* rbar = drain + 1;  // residual chunks, one barrier per epilogue warp
@@ -214,7 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -249,18 +249,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
             for (int t = pair; t < a.total && !*abort_flag; t += npairs) {
                 const Tile ti = decode<kBN>(t, a);
                 const int arow = ti.m0 + (int)rank * kBM;
-                const int brow = kMode == kGated ? ti.n0 : ti.n0 + (int)rank * kBHalf;
+                const int brow = kMode == kGated ? ti.n0 : ti.n0 + (int)rank * C::kBHalf;
                 for (int ks = ti.k0, n; ks < ti.k1; ks += n, ++it) {
                     n = stage_steps(ks, ti, a);
-                    const int s = it % kStages;
-                    if (!wait_or_abort(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag, a.flags)) break;
+                    const int s = it % C::kStages;
+                    if (!wait_or_abort(&empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag, a.flags)) break;
                     const bool seg1 = ks >= a.seg_steps;
                     const CUtensorMap* pA = seg1 || ti.prob ? &mA1 : &mA0;
                     const CUtensorMap* pB = seg1 || (kMode == kGated && rank) ? &mB1 : &mB0;
-                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * n * kStepBytes);
+                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * n * C::kStepBytes);
                     for (int j = 0; j < n; ++j) {
                         const int kc = (ks + j - (seg1 ? a.seg_steps : 0)) * kBK;
-                        uint8_t* sa = smem + s * kStageBytes + j * kStepBytes;
+                        uint8_t* sa = smem + s * C::kStageBytes + j * C::kStepBytes;
                         uint8_t* sb = sa + kABytes;
                         if (kAMN) {
                             tma_load_3d_pair(sa, pA, &full[s], arow, kc, 0);
@@ -270,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                         }
                         if (kBMN) {
 #pragma unroll
-                            for (int i = 0; i < kBHalf / 64; ++i)
+                            for (int i = 0; i < C::kBHalf / 64; ++i)
                                 tma_load_3d_pair(sb + i * kBox, pB, &full[s], brow + 64 * i, kc, 0);
                         } else {
                             tma_load_3d_pair(sb, pB, &full[s], kc, brow, 0);
@@ -280,8 +280,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
             }
             // copies of both CTAs complete on the leader's barriers
             if (leader)
-                for (uint32_t j = (it > (uint32_t)kStages ? it - kStages : 0); j < it; ++j)
-                    drain_wait(&full[j % kStages], (j / kStages) & 1);
+                for (uint32_t j = (it > (uint32_t)C::kStages ? it - C::kStages : 0); j < it; ++j)
+                    drain_wait(&full[j % C::kStages], (j / C::kStages) & 1);
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader)
@@ -289,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
         // the tensor core, so it is kept short: descriptors by addition, no
         // division.  (Testing the next stage's barrier ahead gains nothing.)
         if (leader) {
-            constexpr uint32_t kIdesc = idesc_bf16_major(2 * kBM, kMmaN, kAMN, kBMN);
+            constexpr uint32_t kIdesc = idesc_bf16_major(2 * kBM, C::kMmaN, kAMN, kBMN);
             constexpr uint32_t kStepA = (kAMN ? 2048 : 32) >> 4, kStepB = (kBMN ? 2048 : 32) >> 4;
             const uint32_t base = smem_u32(smem);
             const uint64_t da0 = kAMN ? desc_mnmajor_sw128(base, kBox, 1024) : desc_kmajor_sw128(base);
@@ -311,12 +311,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                     }
                     tc_fence_after();
                     const uint32_t cur = s;
-                    if (++s == kStages) {
+                    if (++s == C::kStages) {
                         s = 0;
                         ph ^= 1;
                     }
-                    uint64_t da = da0 + cur * (kStageBytes >> 4), db = db0 + cur * (kStageBytes >> 4);
-                    for (int j = 0; j < n; ++j, da += kStepBytes >> 4, db += kStepBytes >> 4)
+                    uint64_t da = da0 + cur * (C::kStageBytes >> 4), db = db0 + cur * (C::kStageBytes >> 4);
+                    for (int j = 0; j < n; ++j, da += C::kStepBytes >> 4, db += C::kStepBytes >> 4)
 #pragma unroll
                         for (int kk = 0; kk < kBK / 16; ++kk) {
                             mma_bf16_pair_warp(d, da + kk * kStepA, db + kk * kStepB, kIdesc, sum);
@@ -333,12 +333,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
     } else {
         // ------------------------------------------------ epilogue (both CTAs)
         const int e = warp - 2, q = warp & 3, half = e >> 2;
-        uint8_t* buf_ptr = smem + kEpiOff + (size_t)e * kEpiBuf;
+        uint8_t* buf_ptr = smem + C::kEpiOff + (size_t)e * kEpiBuf;
         const uint32_t buf = smem_u32(buf_ptr);
         constexpr int kHalfCols = kBN / 2;               // output columns of this warp
         constexpr int kChunk = kMode == kF32 ? 32 : 64;  // columns of the staging buffer
         constexpr int kChunks = kHalfCols / kChunk;
-        constexpr int kGroups = 4;  // this warp's accumulator columns, in groups of 32
+        constexpr int kGroups = C::kMmaN / 64;  // this warp's accumulator columns, in groups of 32
         uint32_t tc = 0, rph = 0;
         for (int t = pair; t < a.total; t += npairs, ++tc) {
             const Tile ti = decode<kBN>(t, a);
@@ -381,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
                 // this split's sums of the warp's region, [group][8][lane]
                 // float4; the split that arrives last puts the sum over the
                 // splits, in order, back into TMEM and goes on as for a whole tile
-                constexpr int kRegion = kGroups * 8 * 32, kUnit = 2 * kEpiWarps * kRegion;
+                constexpr int kRegion = 4 * 8 * 32, kUnit = 2 * kEpiWarps * kRegion;
                 float4* parts = reinterpret_cast<float4*>(a.part) + (int64_t)ti.slot * a.splits * kUnit +
                                 (rank * kEpiWarps + e) * kRegion + lane;
 #pragma unroll 1
@@ -614,14 +614,15 @@ struct Maps {
     CUtensorMap A0, A1, B0, B1, D0, D1, D2, R;
 };
 
-template <int kMode, bool kAMN, bool kBMN>
+template <int kMode, bool kAMN, bool kBMN, int kBN>
 cudaError_t launch(const Maps& m, const Args& a, const char* name, cudaStream_t st) {
-    auto* fn = dense_gemm_kernel<kMode, kAMN, kBMN>;
-    cudaError_t e = ensure_smem_attr(fn, kSmem);
+    using C = Cfg<kMode, kBN>;
+    auto* fn = dense_gemm_kernel<kMode, kAMN, kBMN, kBN>;
+    cudaError_t e = ensure_smem_attr(fn, C::kSmem);
     if (e != cudaSuccess) return e;
     const int grid = 2 * std::max(1, std::min(device_sm_count() / 2, a.total));
     trace_before(name, st);
-    e = launch_chained(fn, grid, kThreads, kSmem, 0, st, m.A0, m.A1, m.B0, m.B1, m.D0, m.D1, m.D2, m.R, a);
+    e = launch_chained(fn, grid, kThreads, C::kSmem, 0, st, m.A0, m.A1, m.B0, m.B1, m.D0, m.D1, m.D2, m.R, a);
     trace_after(st);
     return e;
 }
@@ -670,18 +671,33 @@ constexpr int64_t kUnitFloats = 256 * 256;
 constexpr size_t kCounterBytes = (size_t)kDensePairs * 2 * kEpiWarps * sizeof(uint32_t);
 static_assert(kCounterBytes <= kDenseCounterBytes, "counters");
 
+// Time of a tile of 128 columns against one of 256.
+constexpr double kNarrow = 0.65;
 struct Problem {  // M x N outputs over `steps` reduction steps, `problems` times
     int64_t M;
     int N, bn, seg_steps, segs, problems;
     Split split;
     int64_t tiles() const { return (int64_t)cdiv(M, 2 * kBM) * cdiv(N, bn) * problems; }
     TailPlan plan() const { return tail_plan(tiles(), seg_steps * segs, split); }
+    // reduction steps of the busiest pair, a split's overhead among them
+    double pair_steps() const { return (double)(tiles() / kDensePairs) * seg_steps * segs + plan().cost; }
     size_t part_floats() const {
         const TailPlan p = plan();
         return (size_t)p.slots * p.splits * kUnitFloats;
     }
 };
-Problem fwd_problem(int64_t T, int K, int N, bool gated) { return {T, N, gated ? 128 : 256, cdiv(K, kBK), 1, 1, kInKernel}; }
+// The linear forward has column tiles of 256, or of 128 where the finer grid ends
+// sooner: 512 x 4096 -> 4096 takes 19.8 instead of 21.9 us (64 tiles for 74 pairs,
+// not 32), 2048 x 1024 -> 1024 8.6 instead of 10.4; but 4096 x 4096 -> 14336, whose
+// waves are full either way, would take 421 instead of 329.  An input gradient shares
+// the GPU with the weight gradient, which takes up the idle pairs, and gains nothing
+// (2048 x 4096 -> 4096: 112.0 and 112.2 us with and without).
+Problem fwd_problem(int64_t T, int K, int N, bool gated) {
+    const Problem p{T, N, gated ? 128 : 256, cdiv(K, kBK), 1, 1, kInKernel};
+    Problem q = p;
+    q.bn = 128;
+    return !gated && kNarrow * q.pair_steps() < 0.97 * p.pair_steps() ? q : p;
+}
 Problem dgrad_problem(int64_t T, int K, int N, int segs) { return {T, K, 256, cdiv(N, kBK), segs, 1, kInKernel}; }
 Problem wgrad_problem(int64_t T, int K, int N, int problems, bool split) {
     return {N, K, 256, cdiv(T, kBK), 1, problems, split ? kOwnKernel : kWhole};
@@ -708,10 +724,11 @@ Args args_of(const Problem& pr, const DenseWs& ws) {
 
 }  // namespace
 
-double dense_pairs_steps(int64_t T, int N, int64_t k, int segs, bool gated) {
-    const Problem p{T, N, gated ? 128 : 256, cdiv(k, kBK), segs, 1, kInKernel};
-    return (double)(p.tiles() / kDensePairs) * p.seg_steps * segs + p.plan().cost;
+double dense_fwd_pairs_steps(int64_t T, int K, int N, bool gated) {
+    const Problem p = fwd_problem(T, K, N, gated);
+    return p.pair_steps() * (!gated && p.bn == 128 ? kNarrow : 1);
 }
+double dense_dgrad_pairs_steps(int64_t T, int K, int N, int segs) { return dgrad_problem(T, K, N, segs).pair_steps(); }
 static int ctas_of(const Problem& p) {
     const TailPlan t = p.plan();
     return 2 * std::min(kDensePairs, t.full + t.slots * t.splits);
@@ -722,8 +739,7 @@ int dense_wgrad_ctas(int64_t T, int K, int N, int problems, bool split) {
 }
 double dense_wgrad_us(int64_t T, int K, int N, int problems, bool split) {
     const Problem p = wgrad_problem(T, K, N, problems, split);
-    const double steps = (double)(p.tiles() / kDensePairs) * p.seg_steps + p.plan().cost;
-    return 4.5 + std::max(0.33 * steps, (double)problems * N * K * 4 / 5.2e6);
+    return 4.5 + std::max(0.33 * p.pair_steps(), (double)problems * N * K * 4 / 5.2e6);
 }
 size_t dense_fwd_pairs_part_floats(int64_t T, int K, int N, bool gated) {
     return fwd_problem(T, K, N, gated).part_floats();
@@ -738,26 +754,29 @@ size_t dense_wgrad_part_floats(int64_t T, int K, int N, int problems) {
 cudaError_t launch_dense_fwd_pairs(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
                                    const DenseOut& o, const DenseWs& ws, cudaStream_t st) {
     const bool gated = w1 != nullptr;
+    const Problem pr = fwd_problem(T, K, N, gated);
+    const int bhalf = gated ? 128 : pr.bn / 2;
     Maps m;
-    bool ok = make_tile_map(&m.A0, false, x, K, T, 1, kBM) && make_tile_map(&m.B0, false, w0, K, N, 1, kBHalf) &&
+    bool ok = make_tile_map(&m.A0, false, x, K, T, 1, kBM) && make_tile_map(&m.B0, false, w0, K, N, 1, bhalf) &&
               make_tile_map(&m.D0, false, o.y, N, T, 1, 32);
     m.A1 = m.A0;
     m.B1 = m.B0;
     m.D1 = m.D2 = m.R = m.D0;
-    if (gated) ok = ok && make_tile_map(&m.B1, false, w1, K, N, 1, kBHalf);
+    if (gated) ok = ok && make_tile_map(&m.B1, false, w1, K, N, 1, bhalf);
     if (o.z0) ok = ok && make_tile_map(&m.D1, false, o.z0, N, T, 1, 32);
     if (o.z1) ok = ok && make_tile_map(&m.D2, false, o.z1, N, T, 1, 32);
     if (o.res) ok = ok && make_tile_map(&m.R, false, o.res, N, T, 1, 32);
     if (!ok) return cudaErrorInvalidValue;
-    Args a = args_of(fwd_problem(T, K, N, gated), ws);
+    Args a = args_of(pr, ws);
     a.act = o.act;
     a.bias0 = o.bias0;
     a.bias1 = o.bias1;
     a.has_res = o.res != nullptr;
     a.has_z0 = o.z0 != nullptr;
     a.has_z1 = o.z1 != nullptr;
-    if (gated) return launch<kGated, false, false>(m, a, "gated_fwd", st);
-    return launch<kLinear, false, false>(m, a, "linear_fwd", st);
+    if (gated) return launch<kGated, false, false, 128>(m, a, "gated_fwd", st);
+    return pr.bn == 128 ? launch<kLinear, false, false, 128>(m, a, "linear_fwd", st)
+                        : launch<kLinear, false, false, 256>(m, a, "linear_fwd", st);
 }
 
 cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T,
@@ -772,7 +791,7 @@ cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const voi
         ok = ok && make_tile_map(&m.A1, false, dz1, N, T, 1, kBM) && make_tile_map(&m.B1, false, w1, K, N, 1, 64);
     if (!ok) return cudaErrorInvalidValue;
     const Args a = args_of(dgrad_problem(T, K, N, dz1 ? 2 : 1), ws);
-    return launch<kPlain, false, true>(m, a, dz1 ? "gated_dgrad" : "linear_dgrad", st);
+    return launch<kPlain, false, true, 256>(m, a, dz1 ? "gated_dgrad" : "linear_dgrad", st);
 }
 
 cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, int64_t T, int K, int N, void* dw0,
@@ -788,7 +807,8 @@ cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, 
     Args a = args_of(wgrad_problem(T, K, N, dz1 ? 2 : 1, plan.split), ws);
     a.late_wait = plan.beside;
     const char* name = dz1 ? "gated_wgrad" : "linear_wgrad";
-    const cudaError_t e = f32 ? launch<kF32, true, true>(m, a, name, st) : launch<kPlain, true, true>(m, a, name, st);
+    const cudaError_t e =
+        f32 ? launch<kF32, true, true, 256>(m, a, name, st) : launch<kPlain, true, true, 256>(m, a, name, st);
     if (e != cudaSuccess || a.total == a.full || a.counters) return e;
     const dim3 grid((a.total - a.full) / a.splits, 2 * kEpiWarps * 4);
     trace_before("wgrad_sum", st);

@@ -412,11 +412,11 @@ cudaError_t launch_dgrad_skinny(const Geometry& g, const void* dz0, const void* 
 }
 
 // The pair kernel's estimated time for T rows, N outputs and a reduction of k (in
-// `segs` segments): 6.5 us and 0.34 per reduction step of the rounds of tiles,
-// or its operands at 5.2 TB/s.
-double pairs_us(int64_t T, int N, int64_t k, int segs, bool gated) {
+// `segs` segments): 6.5 us and 0.34 per reduction step of the rounds of tiles
+// (`steps`), or its operands at 5.2 TB/s.
+double pairs_us(int64_t T, int N, int64_t k, int segs, bool gated, double steps) {
     const double bytes = ((gated ? 2 : 1) * (double)N + (double)T) * k * segs * 2;
-    return 6.5 + std::max(bytes / 5.2e6, 0.34 * dense_pairs_steps(T, N, k, segs, gated));
+    return 6.5 + std::max(bytes / 5.2e6, 0.34 * steps);
 }
 
 // Which form a product takes: few rows in this geometry, or pairs (few = false).
@@ -431,15 +431,18 @@ struct Choice {
 // against 20.4 us on 2880 -> 2880 (pairs: 12 tiles for 74 pairs); at T = 256 it
 // takes 39.7 against 31.6 us on 4096 -> 14336, where 112 feature tiles read the
 // tokens 112 times.
-Choice choose(int64_t T, int N, int64_t k, int segs, bool gated, int pair_ctas, int64_t most_ctas = kAnyCtas) {
-    Choice c{false, {}, pair_ctas, pairs_us(T, N, k, segs, gated)};
+Choice choose(int64_t T, int N, int64_t k, int segs, bool gated, double pair_steps, int pair_ctas,
+              int64_t most_ctas = kAnyCtas) {
+    Choice c{false, {}, pair_ctas, pairs_us(T, N, k, segs, gated, pair_steps)};
     if (T > 65535 * 16) return c;  // the grid's second dimension counts token tiles
     const Geometry g = best_geometry(T, N, k, segs, gated, most_ctas);
     if (g.tn && (g.us < c.us || c.ctas > most_ctas)) c = Choice{true, g, g.ctas, g.us};
     return c;
 }
 
-Choice choose_fwd(int64_t T, int K, int N, bool gated) { return choose(T, N, K, 1, gated, 0); }
+Choice choose_fwd(int64_t T, int K, int N, bool gated) {
+    return choose(T, N, K, 1, gated, dense_fwd_pairs_steps(T, K, N, gated), 0);
+}
 
 // The input gradient's form, and how the weight gradient (where one follows)
 // runs.  Beside an input gradient that leaves SMs idle the weight gradient starts
@@ -454,14 +457,15 @@ struct DgradPlan {
 };
 DgradPlan plan_dgrad(int64_t T, int K, int N, int segs, bool with_wgrad) {
     const int pair_ctas = dense_dgrad_pairs_ctas(T, K, N, segs);
-    const Choice alone = choose(T, K, N, segs, false, pair_ctas);
+    const double pair_steps = dense_dgrad_pairs_steps(T, K, N, segs);
+    const Choice alone = choose(T, K, N, segs, false, pair_steps, pair_ctas);
     DgradPlan best{alone, {true, with_wgrad && alone.ctas <= 140}};
     if (!with_wgrad) return best;
     double best_us = alone.us + dense_wgrad_us(T, K, N, segs, true);
     for (int split = 0; split < 2; ++split) {
         const int64_t room = 148 - dense_wgrad_ctas(T, K, N, segs, split);
         if (room < 16) continue;
-        const Choice fit = choose(T, K, N, segs, false, pair_ctas, room);
+        const Choice fit = choose(T, K, N, segs, false, pair_steps, pair_ctas, room);
         const double us = std::max(fit.us, dense_wgrad_us(T, K, N, segs, split)) + 1;
         if (fit.ctas <= room && us < best_us) {
             best = {fit, {split != 0, true}};

@@ -225,6 +225,13 @@ def test_linear_forward(gpu_lib, T, K, N, act):
     assert moe.moe_dense_get_device_status(ws) == 0
 
 
+# Fewer tiles than CTA pairs, in narrow tiles: whole, ragged, and with the last ones
+# split along the reduction.
+@pytest.mark.parametrize("T,K,N", [(2048, 1024, 1024), (1500, 1000, 1016), (600, 4096, 3304)])
+def test_linear_forward_few_tiles(gpu_lib, T, K, N):
+    test_linear_forward(gpu_lib, T, K, N, "gelu_tanh")
+
+
 LIN_BWD = [(1, 64, 8, "silu"), (1, 264, 4096, "none"), (7, 136, 72, "gelu"), (64, 520, 264, "relu"),
            (65, 72, 200, "gelu_tanh"), (257, 264, 136, "none"), (300, 2040, 72, "silu"), (72, 2040, 2200, "none"),
            (2100, 264, 328, "gelu"), (5000, 72, 136, "none"), (1031, 520, 8, "silu"), (2200, 2040, 72, "none"),
