@@ -510,7 +510,8 @@ moe_status_t moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const
  *   MOE_NORM_RMS), rstd [T] as the forward wrote them; d_residual [T, H] or
  *   NULL: the gradient that reaches x past the norm; d_weight, d_bias [H]
  *   float32 or NULL to skip.  dx may be d_residual, or dy when both have the
- *   same type.  ws: moe_norm_workspace_size(cfg) bytes (partial sums).
+ *   same type.  ws: moe_norm_workspace_size(cfg) bytes, 256-byte aligned
+ *   (partial sums, behind MOE_DENSE_WS_HEADER bytes that are left alone).
  */
 size_t moe_norm_workspace_size(const moe_norm_config_t* cfg);
 moe_status_t moe_norm_backward(const moe_norm_config_t* cfg, const void* dy, const void* x, const float* weight,
@@ -531,9 +532,9 @@ typedef struct {
  * and counters, must be zero before the workspace's first use; every call
  * leaves the counters zero.  After a call whose flags
  * (moe_dense_get_device_status) report a timeout, that query has cleared them
- * again.  One workspace may serve calls of different sizes, one after the
- * other. */
-#define MOE_DENSE_WS_HEADER 9984
+ * again.  One workspace may serve calls of different sizes, and
+ * moe_norm_backward, one after the other. */
+#define MOE_DENSE_WS_HEADER 5120
 size_t moe_linear_workspace_size(const moe_dense_config_t* cfg);
 size_t moe_linear_backward_workspace_size(const moe_dense_config_t* cfg);
 size_t moe_gated_workspace_size(const moe_dense_config_t* cfg);

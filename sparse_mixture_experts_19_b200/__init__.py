@@ -25,7 +25,7 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "M
 DEVFLAG_BAD_EXPERT_INDEX = 0x1
 DEVFLAG_WAIT_TIMEOUT = 0x2
 ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
-DENSE_WS_HEADER = 9984  # MOE_DENSE_WS_HEADER
+DENSE_WS_HEADER = 5120  # MOE_DENSE_WS_HEADER
 NORMS = {"layer": 0, "rms": 1}
 
 

@@ -29,7 +29,7 @@ moe_status_t check_norm(const moe_norm_config_t* c) {
 }
 
 size_t norm_ws_bytes(const moe_norm_config_t* c) {
-    return align_up(sizeof(float) * 2 * c->H * (c->T > 0 ? norm_bwd_blocks(c->T) : 1));
+    return MOE_DENSE_WS_HEADER + align_up(sizeof(float) * 2 * c->H * (c->T > 0 ? norm_bwd_blocks(c->T) : 1));
 }
 
 moe_status_t check_dense(const moe_dense_config_t* c) {
@@ -47,10 +47,9 @@ moe_status_t check_dense(const moe_dense_config_t* c) {
 
 // Pieces of a dense workspace.
 struct DensePlan {
-    // flags and both products' counters first: the header that
-    // moe_dense_get_device_status clears
+    // flags and counters first: the header that moe_dense_get_device_status clears
     DenseWs ws;   // the forward product, or the input gradient
-    DenseWs wws;  // the weight gradient
+    DenseWs wws;  // the weight gradient (no counters: a second kernel adds its splits)
     bf16* dz0;   // [T, N], unless the linear layer has no activation
     bf16* dz1;   // gated
     float* sums; // partial bias gradients
@@ -69,7 +68,6 @@ void make_dense_plan(const moe_dense_config_t* c, bool gated, bool backward, voi
     p->ws.flags = (int32_t*)take(64);
     p->ws.counters = (uint32_t*)take(kDenseCounterBytes);
     p->wws.flags = p->ws.flags;
-    p->wws.counters = (uint32_t*)take(kDenseCounterBytes);
     const int two = gated ? 2 : 1;
     if (backward && c->T > 0) {
         const size_t tn = (size_t)c->T * c->N;
@@ -187,7 +185,8 @@ moe_status_t moe_norm_backward(const moe_norm_config_t* cfg, const void* dy, con
     a.rstd = rstd;
     a.d_res = d_residual;
     a.dx = dx;
-    a.part = d_weight || d_bias ? (float*)ws : nullptr;
+    // behind the header of the dense calls, which may share the workspace
+    a.part = d_weight || d_bias ? (float*)((char*)ws + MOE_DENSE_WS_HEADER) : nullptr;
     a.dw_out = d_weight;
     a.db_out = d_bias;
     CUDA_TRY(launch_norm_bwd(a, cfg->dtype == MOE_F32, cfg->dy_dtype == MOE_F32, st), "norm_bwd");
@@ -248,6 +247,10 @@ moe_status_t moe_linear_backward(const moe_dense_config_t* cfg, const void* dy, 
     if (act) REQUIRE_PTR(z);
     NOT_SAME(dx, dy);
     NOT_SAME(dx, x);
+    NOT_SAME(dx, w);
+    NOT_SAME(d_w, x);
+    NOT_SAME(d_w, w);
+    NOT_SAME(d_w, dx);
     const bf16* dz = act ? p.dz0 : (const bf16*)dy;
     if (d_bias || (act && (dx || d_w))) {
         DenseDzArgs a{};
@@ -334,6 +337,14 @@ moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, c
         REQUIRE_PTR(w_up);
     }
     NOT_SAME(dx, x);
+    NOT_SAME(dx, w_gate);
+    NOT_SAME(dx, w_up);
+    for (const void* d_w : {d_w_gate, d_w_up}) {
+        NOT_SAME(d_w, x);
+        NOT_SAME(d_w, w_gate);
+        NOT_SAME(d_w, w_up);
+        NOT_SAME(d_w, dx);
+    }
     DenseDzArgs a{};
     a.T = cfg->T;
     a.N = cfg->N;
@@ -359,13 +370,13 @@ moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, c
 moe_status_t moe_dense_get_device_status(void* ws, size_t ws_bytes, moe_stream_t stream, int32_t* flags_out) {
     if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
     if ((uintptr_t)ws % kWsAlign) return fail(MOE_ERR_WORKSPACE, "workspace not %d-byte aligned", kWsAlign);
-    static_assert(MOE_DENSE_WS_HEADER == kWsAlign + 2 * kDenseCounterBytes, "workspace header");
+    static_assert(MOE_DENSE_WS_HEADER == kWsAlign + kDenseCounterBytes, "workspace header");
     if (ws_bytes < MOE_DENSE_WS_HEADER)
         return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %d", ws_bytes, MOE_DENSE_WS_HEADER);
     const moe_status_t s = read_device_flags((int32_t*)ws, (cudaStream_t)stream, flags_out);
     // a call that gave up may have left its counters counting
     if (s == MOE_ERR_DEVICE_CHECK)
-        CUDA_TRY(cudaMemsetAsync((char*)ws + kWsAlign, 0, 2 * kDenseCounterBytes, (cudaStream_t)stream), "counters clear");
+        CUDA_TRY(cudaMemsetAsync((char*)ws + kWsAlign, 0, kDenseCounterBytes, (cudaStream_t)stream), "counters clear");
     return s;
 }
 

@@ -96,6 +96,10 @@ def test_linear_pointers(lib):
     assert lib.moe_linear_backward(r, P, None, P, P, 2 * P, 3 * P, None, P, BIG, None) == 1
     assert lib.moe_linear_backward(r, P, P, None, P, 2 * P, 3 * P, None, P, BIG, None) == 1
     assert lib.moe_linear_backward(r, P, P, P, P, P, 3 * P, None, P, BIG, None) == 1  # dx is dy
+    # dx is w, d_w is x, w or dx
+    assert lib.moe_linear_backward(r, P, 2 * P, 3 * P, P, 3 * P, 4 * P, None, P, BIG, None) == 1
+    for d_w in (2 * P, 3 * P, 5 * P):
+        assert lib.moe_linear_backward(r, P, 2 * P, 3 * P, P, 5 * P, d_w, None, P, BIG, None) == 1
 
 
 def test_gated_pointers(lib):
@@ -109,6 +113,11 @@ def test_gated_pointers(lib):
     args = [P, P, P, P, P, P, 2 * P, 3 * P, None, None, None]
     assert lib.moe_gated_backward(r, *args, P, BIG, None) == 1  # one weight gradient alone
     assert b"go together" in lib.moe_last_error()
+    # dx is w_gate; d_w_up is x, w_gate, w_up or dx
+    back = [P, 2 * P, 3 * P, 4 * P, P, P, 5 * P, 6 * P, 7 * P, None, None]
+    for i, v in ((6, 3 * P), (8, 2 * P), (8, 3 * P), (8, 4 * P), (8, 5 * P)):
+        assert lib.moe_gated_backward(r, *[v if j == i else a for j, a in enumerate(back)], P, BIG, None) == 1
+        assert b"the same tensor" in lib.moe_last_error()
 
 
 def test_norm_pointers(lib):

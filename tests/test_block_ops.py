@@ -225,11 +225,18 @@ def test_linear_forward(gpu_lib, T, K, N, act):
     assert moe.moe_dense_get_device_status(ws) == 0
 
 
-# Fewer tiles than CTA pairs, in narrow tiles: whole, ragged, and with the last ones
-# split along the reduction.
+# Fewer tiles than CTA pairs: narrow tiles, whole and ragged ones.
 @pytest.mark.parametrize("T,K,N", [(2048, 1024, 1024), (1500, 1000, 1016), (600, 4096, 3304)])
 def test_linear_forward_few_tiles(gpu_lib, T, K, N):
     test_linear_forward(gpu_lib, T, K, N, "gelu_tanh")
+
+
+# The last wave's tiles split along the reduction, and added in the kernel.
+@pytest.mark.parametrize("T,K,N", [(1500, 2880, 3304), (1030, 3200, 4104), (300, 18432, 4944)])
+def test_linear_forward_split_tiles(gpu_lib, T, K, N):
+    moe = gpu_lib
+    assert moe.moe_linear_workspace_size(moe.dense_config(T, K, N)) > moe.DENSE_WS_HEADER
+    test_linear_forward(moe, T, K, N, "silu")
 
 
 LIN_BWD = [(1, 64, 8, "silu"), (1, 264, 4096, "none"), (7, 136, 72, "gelu"), (64, 520, 264, "relu"),
@@ -278,6 +285,10 @@ def test_linear_backward(gpu_lib, T, K, N, act, grad):
 
 
 # ----------------------------------------------------------------- gated
+def test_linear_backward_split_tiles(gpu_lib):
+    test_linear_backward(gpu_lib, 1500, 4104, 4096, "none", "bf16")
+
+
 GATED = [(1, 64, 8), (1, 1024, 264), (6, 72, 136), (17, 520, 128), (128, 200, 328), (129, 264, 1032), (256, 72, 72),
          (257, 1032, 136), (300, 8, 520), (700, 328, 1000)]
 
@@ -317,6 +328,13 @@ def test_gated_forward(gpu_lib, T, K, N, act):
         elif not use_b:
             assert torch.equal(first, h), "keeping g changes h"
     assert moe.moe_dense_get_device_status(ws) == 0
+
+
+def test_gated_forward_split_tiles(gpu_lib):
+    moe = gpu_lib
+    T, K, N = 1030, 3200, 2056
+    assert moe.moe_gated_workspace_size(moe.dense_config(T, K, N)) > moe.DENSE_WS_HEADER
+    test_gated_forward(moe, T, K, N, "silu")
 
 
 GATED_BWD = [(1, 64, 8, "silu"), (3, 4096, 264, "silu"), (65, 264, 72, "gelu"), (256, 136, 520, "relu"),
@@ -361,6 +379,10 @@ def test_gated_backward(gpu_lib, T, K, N, act, grad):
     assert torch.equal(dbu2, dbu)
     within(dx2, dx_ref, dx_tol, "dx alone")
     assert moe.moe_dense_get_device_status(ws) == 0
+
+
+def test_gated_backward_split_tiles(gpu_lib):
+    test_gated_backward(gpu_lib, 1030, 4104, 2056, "silu", "f32")
 
 
 # ----------------------------------------------------- activations far out
@@ -413,14 +435,15 @@ def test_repeatable_and_other_stream(gpu_lib):
     """The same bits again, and on a stream other than the current one."""
     moe, g = gpu_lib, gen_of(11)
     x, w, wu = rnd(g, 300, 520), rnd(g, 264, 520, scale=0.05), rnd(g, 264, 520, scale=0.05)
+    few = x[:9].clone()
     a = moe.gated(x, w, wu)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
     b = moe.gated(x, w, wu, stream=st)
-    y = moe.linear(x[:9].clone(), w, stream=st)
+    y = moe.linear(few, w, stream=st)
     st.synchronize()
     assert torch.equal(a, b) and torch.equal(a, moe.gated(x, w, wu))
-    assert torch.equal(y, moe.linear(x[:9].clone(), w))
+    assert torch.equal(y, moe.linear(few, w))
 
 
 def test_captured_and_replayed(gpu_lib):
@@ -498,6 +521,25 @@ def test_one_workspace_for_several_sizes(gpu_lib):
                 want[T] = own
             assert all(torch.equal(a, b) for a, b in zip(out, want[T])), (rep, T)
     assert (ws[:moe.DENSE_WS_HEADER] == 0).all()
+
+
+def test_one_workspace_for_the_block(gpu_lib):
+    """The norm's backward pass leaves the header of a workspace that the dense
+    calls use too, whose forward here splits its tiles (counters)."""
+    moe, g = gpu_lib, gen_of(16)
+    T, K, N = 1500, 2880, 3304
+    x, w = rnd(g, T, K), rnd(g, N, K, scale=K ** -0.5)
+    cfg, ncfg = moe.dense_config(T, K, N), moe.norm_config(T, K)
+    ws = moe._new_ws(max(moe.moe_linear_workspace_size(cfg), moe.moe_norm_workspace_size(ncfg)), "cuda")
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    moe.norm(x, mean_out=mean, rstd_out=rstd)
+    want = moe.linear(x, w)
+    for _ in range(2):
+        dx, dw, db = torch.empty_like(x), torch.empty(K, device="cuda"), torch.empty(K, device="cuda")
+        moe.moe_norm_backward(ncfg, x, x, None, mean, rstd, None, dx, dw, db, ws)
+        assert (ws[:moe.DENSE_WS_HEADER] == 0).all()
+        assert torch.equal(moe.linear(x, w, ws=ws), want)
+    assert moe.moe_dense_get_device_status(ws) == 0
 
 
 def test_offsets_past_32_bits(gpu_lib):
