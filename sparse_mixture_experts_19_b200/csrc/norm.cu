@@ -12,7 +12,8 @@
 // built around bytes in flight: one CTA per SM, whose 16 warps form groups of
 // W warps, one row per group at a time.  Each group has a ring of S row slots
 // in shared memory that one thread fills with bulk copies (rows are
-// contiguous), up to 200 KB per SM on their way whatever the registers hold.
+// contiguous), up to 80 KB (backward: 200 KB) per SM on their way whatever the
+// registers hold.
 // A row is read from HBM once; its statistics (forward: the mean, then the
 // squared deviations from it, so no cancellation; backward: the two sums) are
 // warp sums joined through shared memory with one barrier of the group each,
@@ -38,6 +39,11 @@ using namespace sm100;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRingBytes = 200 * 1024;
+// The forward's ring (two rows per group at least): 80 KB per SM are what HBM's
+// latency asks for, and reading further ahead of the writes mostly costs (bf16,
+// RMS form: 16384 rows of 2880 take 32.5 us with 80 KB and 35.2 with 200, 16384 of
+// 4096 42.7 and 47.4; but 65536 of 1024 47.3 and 45.0).
+constexpr int kFwdRingBytes = 80 * 1024;
 constexpr int kMaxSlots = 8;
 constexpr int kMaxVpt = 4;  // groups of 8 elements per thread (or 2)
 
@@ -217,17 +223,15 @@ __global__ void __launch_bounds__(kThreads, 1) norm_fwd_kernel(const NormArgs a,
     for (int64_t row = first; row < a.T; row += step) {
         const float bad = slot_wait(&bar[s], ph);
         const X* src = reinterpret_cast<const X*>(ring + s * geo.slot_bytes);
-        Raw8<X> raw[kVpt];
+        float val[kVpt][8];  // the row, then its deviations from the mean
         float sum[2] = {bad, 0.f};
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
             const int c = (i * g.threads + g.t) * 8;
             if (c < a.H) {
-                raw[i].load(src + c);
-                float v[8];
-                raw[i].get(v);
+                load8(src + c, val[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j & 1] += v[j];
+                for (int j = 0; j < 8; ++j) sum[j & 1] += val[i][j];
             }
         }
         float mu = bad;
@@ -239,11 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_fwd_kernel(const NormArgs a,
 #pragma unroll
         for (int i = 0; i < kVpt; ++i)
             if ((i * g.threads + g.t) * 8 < a.H) {
-                float v[8];
-                raw[i].get(v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float d = v[j] - mu;
+                    const float d = val[i][j] -= mu;
                     sum[j & 1] = fmaf(d, d, sum[j & 1]);
                 }
             }
@@ -261,9 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) norm_fwd_kernel(const NormArgs a,
             const int c = (i * g.threads + g.t) * 8;
             if (c < a.H) {
                 float v[8];
-                raw[i].get(v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = fmaf((v[j] - mu) * r, w[i][j], b[i][j]);
+                for (int j = 0; j < 8; ++j) v[j] = fmaf(val[i][j] * r, w[i][j], b[i][j]);
                 store8(y + c, v);
             }
         }
@@ -453,17 +454,18 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, i
 }
 
 // Warps per row: as few as hold the row in `vpt` groups of 8 elements per
-// thread, so that a CTA has several independent rows in flight; more when the
-// slots of a group would otherwise be fewer than three (two rows ahead of the
-// one being worked on).
-Geo geo_of(int H, int slot_bytes, int vpt) {
+// thread, so that a CTA has several independent rows in flight; more when
+// `least` slots for every group would not fit.  Slots as the ring of `bytes`
+// holds, `least` of them at any rate.
+Geo geo_of(int H, int slot_bytes, int vpt, int bytes, int least) {
     Geo g;
     g.slot_bytes = slot_bytes;
     g.W = 1;
     while (g.W * 32 * 8 * vpt < H) g.W *= 2;
-    auto slots = [&] { return std::min(kMaxSlots, kRingBytes / (kWarps / g.W) / slot_bytes); };
-    while (g.W < kWarps && slots() < 3) g.W *= 2;
-    g.S = std::max(1, slots());
+    auto slots = [&](int ring) { return ring / (kWarps / g.W) / slot_bytes; };
+    while (g.W < kWarps && slots(kRingBytes) < least) g.W *= 2;
+    if (g.W >= 8) least = std::max(least, 3);
+    g.S = std::max(1, std::min({kMaxSlots, slots(kRingBytes), std::max(least, slots(bytes))}));
     return g;
 }
 
@@ -507,7 +509,7 @@ cudaError_t launch_fwd(const NormArgs& a, const Geo& g, cudaStream_t st) {
 
 template <typename X>
 cudaError_t launch_fwd(const NormArgs& a, cudaStream_t st) {
-    const Geo g = geo_of(a.H, a.H * (int)sizeof(X), kMaxVpt);
+    const Geo g = geo_of(a.H, a.H * (int)sizeof(X), kMaxVpt, kFwdRingBytes, 2);
     switch (g.W) {
         case 1: return launch_fwd<X, 1>(a, g, st);
         case 2: return launch_fwd<X, 2>(a, g, st);
@@ -522,7 +524,7 @@ cudaError_t launch_bwd(const NormArgs& a, cudaStream_t st) {
     // two groups of elements per thread up to H = 8192: with four, the sums of
     // both weight gradients alone take half of the registers
     const bool two = a.H <= kWarps * 32 * 8 * 2;
-    const Geo g = geo_of(a.H, a.H * (int)(sizeof(X) * (a.d_res ? 2 : 1) + sizeof(G)), two ? 2 : kMaxVpt);
+    const Geo g = geo_of(a.H, a.H * (int)(sizeof(X) * (a.d_res ? 2 : 1) + sizeof(G)), two ? 2 : kMaxVpt, kRingBytes, 3);
     const char* name = "norm_bwd";
     if (!two) return launch(norm_bwd_kernel<X, G, kMaxVpt, 16, kDb>, a, g, name, st);
     switch (g.W) {
