@@ -7,8 +7,24 @@
 
 namespace moe {
 
-// p(z) = 1 / (1 + e^-z) through the fast exponential: an infinite e^-z gives 0.
-__device__ __forceinline__ float sigmoid_f32(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// The special function unit's 2^x and 1/x (2 and 1 units in the last place), with
+// results below the normal range as 0: the forms that keep those take three
+// instructions more each (GELU forward, 8191 x 2880 -> 2880: 109.9 us with those,
+// 106.3 with these).
+__device__ __forceinline__ float exp2_f32(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_f32(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// p(z) = 1 / (1 + e^-z): an infinite e^-z gives 0.
+__device__ __forceinline__ float sigmoid_f32(float z) { return rcp_f32(1.f + exp2_f32(-kLog2e * z)); }
 
 // sqrt(2 / pi) (z + 0.044715 z^3), doubled: tanh-form GELU is z sigmoid(this).
 __device__ __forceinline__ float gelu_tanh_arg(float z) {
@@ -21,8 +37,8 @@ __device__ __forceinline__ float gelu_tanh_arg(float z) {
 // matrix product's epilogue (10 us of a 30 us call).  In the lower tail Phi is
 // this product itself, not one minus it, so it falls off to zero as it should.
 __device__ __forceinline__ float normal_cdf_f32(float z, float& gauss) {
-    const float t = __fdividef(1.f, fmaf(0.23164189f, fabsf(z), 1.f));
-    gauss = __expf(-0.5f * z * z);
+    const float t = rcp_f32(fmaf(0.23164189f, fabsf(z), 1.f));
+    gauss = exp2_f32(-0.5f * kLog2e * z * z);
     float p = fmaf(1.061405429f, t, -1.453152027f);
     p = fmaf(p, t, 1.421413741f);
     p = fmaf(p, t, -0.284496736f);
@@ -31,8 +47,7 @@ __device__ __forceinline__ float normal_cdf_f32(float z, float& gauss) {
     return z < 0.f ? q : 1.f - q;
 }
 
-// act(z).  __fdividef(1, y) is 0 for y above 2^126, where the sigmoid is below
-// every float32 normal anyway.  ReLU keeps a NaN.
+// act(z).  ReLU keeps a NaN.
 template <int kAct>
 __device__ __forceinline__ float act_value(float z) {
     if (kAct == MOE_ACT_SILU) return z * sigmoid_f32(z);
