@@ -480,6 +480,8 @@ class _Call:
         """(pointer, bytes) of a workspace on the current device."""
         if ws is None or isinstance(ws, int):
             return _ws(ws)
+        if ws.get_device() == self.dev and ws.is_contiguous():
+            return ws.data_ptr(), ws.nbytes
         if ws.is_cuda and ws.get_device() != self.dev:
             raise MoeError(1, f"ws is on {ws.device}, not on the current device")
         return _ptr(ws), ws.nbytes
@@ -492,13 +494,18 @@ class _Call:
         return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+_torch_types: dict = {}
+
+
 def _torch_type(code: int):
     """The torch dtype of a MOE_* dtype."""
-    import torch
+    if not _torch_types:
+        import torch
 
-    if code not in (MOE_F32, MOE_BF16):
+        _torch_types.update({MOE_F32: torch.float32, MOE_BF16: torch.bfloat16})
+    if code not in _torch_types:
         raise MoeError(1, f"dtype = {code} unknown")
-    return torch.bfloat16 if code == MOE_BF16 else torch.float32
+    return _torch_types[code]
 
 
 def _sized(size_fn, cfg) -> int:

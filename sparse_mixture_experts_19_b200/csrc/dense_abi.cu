@@ -86,12 +86,11 @@ moe_status_t dense_plan_for(const moe_dense_config_t* c, bool gated, bool backwa
                             DensePlan* p) {
     moe_status_t s = check_dense(c);
     if (s != MOE_OK) return s;
-    make_dense_plan(c, gated, backward, nullptr, p);
+    make_dense_plan(c, gated, backward, ws, p);
     if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
     if ((uintptr_t)ws % kWsAlign) return fail(MOE_ERR_WORKSPACE, "workspace not %d-byte aligned", kWsAlign);
     if (ws_bytes < p->bytes)
         return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, p->bytes);
-    make_dense_plan(c, gated, backward, ws, p);
     return MOE_OK;
 }
 
