@@ -314,6 +314,9 @@ struct Geometry {
 // rms error 9%): a step is the slowest of issuing it (0.29 us), its MMAs and its
 // bytes at the rate that the SMs draw from L2 together; then the partial sums
 // that come from peers, and the tile's way out of TMEM and through the epilogue.
+// The weights come from HBM at 6.2 TB/s for one token tile, at 5.0 for several
+// (gate/up, 64 rows: 14336 -> 4096 takes 42.4 us in one tile and 52.3 in two, but
+// 2880 -> 2880, bound by its steps, 13.2 and 12.0).
 Geometry geometry(int64_t T, int N, int64_t k, int steps, int acc, int tn, int64_t most_ctas) {
     // clusters of s CTAs with 209 KB of shared memory each that a B200 holds at
     // once (a cluster stays inside a GPC), a little below what it reports
@@ -323,10 +326,11 @@ Geometry geometry(int64_t T, int N, int64_t k, int steps, int acc, int tn, int64
     for (int s = 2; s <= 8; ++s)
         if (tiles <= kFit[s] && tiles * s <= most_ctas && steps >= 4 * s) g.splits = s;
     g.ctas = tiles * g.splits;
+    const double rate = T <= tn ? 6.2e6 : 5.0e6;  // of the weights, read once or again by each token tile
     const double ctas = (double)g.ctas, rounds = (double)cdiv(g.ctas, 148), cols = tn * acc;
     const double step =
         std::max({0.29, 0.0016 * cols, (acc * kABytes + tn * kBK * 2) * std::min(ctas, 148.0) / 17.6e6});
-    const double stream = std::max(rounds * cdiv(steps, g.splits) * step, acc * (double)N * k * 2 / 5.2e6);
+    const double stream = std::max(rounds * cdiv(steps, g.splits) * step, acc * (double)N * k * 2 / rate);
     g.us = 2.8 + stream + 0.016 * cols * (g.splits - 1) / g.splits + rounds * cols * (0.0094 + 0.017 / g.splits);
     return g;
 }
@@ -427,9 +431,9 @@ struct Choice {
     double us;
 };
 
-// The form whose estimated time is less.  At T = 128 the few-row form takes 10.0
-// against 20.4 us on 2880 -> 2880 (pairs: 12 tiles for 74 pairs); at T = 256 it
-// takes 39.7 against 31.6 us on 4096 -> 14336, where 112 feature tiles read the
+// The form whose estimated time is less.  At T = 128 the few-row form takes 9.7
+// against 14.9 us on 2880 -> 2880 (pairs: 23 tiles for 74 pairs); at T = 256 it
+// takes 42.8 against 33.5 us on 4096 -> 14336, where 112 feature tiles read the
 // tokens 112 times.
 Choice choose(int64_t T, int N, int64_t k, int segs, bool gated, double pair_steps, int pair_ctas,
               int64_t most_ctas = kAnyCtas) {
