@@ -8,7 +8,7 @@
 // weight bytes.  A CTA owns one tile and one share of the reduction: a cluster
 // of S <= 8 CTAs splits the reduction (enough clusters to cover the SMs when
 // the output has few feature tiles), and each streams its share through a TMA
-// ring of up to 200 KB (weights 16 KB per 64-deep step, read once).  Then CTA r
+// ring of up to 208 KB (weights 16 KB per 64-deep step, read once).  Then CTA r
 // of the cluster finishes the r-th share of the tokens: it adds the S partial
 // sums, its own and the peers' through distributed shared memory, all S loads
 // of an element in flight at once (one at a time they took 4 us of a 9 us call
@@ -52,6 +52,7 @@ struct Args {
     int T, N;        // tokens, output features
     int tn;          // tokens per tile (multiple of 16)
     int stages;
+    int per;         // reduction steps in a stage: the kernel's kPer
     int seg_steps, steps;
     int splits;      // CTAs per cluster
     int act;
@@ -80,7 +81,7 @@ __device__ __forceinline__ void store4(bf16* p, const float (&v)[4]) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-template <bool kGated, bool kAMN>
+template <bool kGated, bool kAMN, int kPer>
 __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_constant__ CUtensorMap mA0,
                                                                    const __grid_constant__ CUtensorMap mA1,
                                                                    const __grid_constant__ CUtensorMap mB0,
@@ -99,29 +100,35 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
     const int n0 = (int)(blockIdx.x / a.splits) * 128, t0 = (int)blockIdx.y * a.tn;
     const int ks0 = (int)((int64_t)a.steps * rank / a.splits), ks1 = (int)((int64_t)a.steps * (rank + 1) / a.splits);
     const int b_bytes = a.tn * kBK * 2;
-    const int stage_bytes = (kGated ? 2 : 1) * kABytes + b_bytes;
+    const int step_bytes = (kGated ? 2 : 1) * kABytes + b_bytes, stage_bytes = kPer * step_bytes;
     constexpr int kAcc = kGated ? 2 : 1;
     const int tokens = min(a.tn, a.T - t0);
     // tokens CTA r of the cluster finishes
     auto share = [&](int r) { return tokens * r / a.splits; };
     const int tk0 = share((int)rank), tk1 = share((int)rank + 1);
-    auto load_step = [&](int ks, int s) {
+    // steps of the stage that starts at ks: fewer at the end of a segment or of the share
+    auto steps_of = [&](int ks) { return kPer == 2 && ks + 1 < ks1 && ks + 1 != a.seg_steps ? 2 : 1; };
+    auto load_stage = [&](int ks, int s) {
         const bool seg1 = ks >= a.seg_steps;
-        const int kc = (seg1 ? ks - a.seg_steps : ks) * kBK;
-        uint8_t* sa = smem + s * stage_bytes;
-        uint8_t* sb = sa + (kGated ? 2 : 1) * kABytes;
-        mbar_arrive_expect_tx(&full[s], stage_bytes);
-        if (kAMN) {
-            const CUtensorMap* pA = seg1 ? &mA1 : &mA0;
-            tma_load_3d(sa, pA, &full[s], n0, kc, 0);
-            tma_load_3d(sa + kBox, pA, &full[s], n0 + 64, kc, 0);
-        } else {
-            tma_load_3d(sa, &mA0, &full[s], kc, n0, 0);
-            if (kGated) tma_load_3d(sa + kABytes, &mA1, &full[s], kc, n0, 0);
+        const int n = steps_of(ks);
+        mbar_arrive_expect_tx(&full[s], n * step_bytes);
+        for (int j = 0; j < n; ++j) {
+            const int kc = (seg1 ? ks + j - a.seg_steps : ks + j) * kBK;
+            uint8_t* sa = smem + s * stage_bytes + j * step_bytes;
+            uint8_t* sb = sa + (kGated ? 2 : 1) * kABytes;
+            if (kAMN) {
+                const CUtensorMap* pA = seg1 ? &mA1 : &mA0;
+                tma_load_3d(sa, pA, &full[s], n0, kc, 0);
+                tma_load_3d(sa + kBox, pA, &full[s], n0 + 64, kc, 0);
+            } else {
+                tma_load_3d(sa, &mA0, &full[s], kc, n0, 0);
+                if (kGated) tma_load_3d(sa + kABytes, &mA1, &full[s], kc, n0, 0);
+            }
+            tma_load_3d(sb, seg1 ? &mB1 : &mB0, &full[s], kc, t0, 0);
         }
-        tma_load_3d(sb, seg1 ? &mB1 : &mB0, &full[s], kc, t0, 0);
+        return n;
     };
-    const int first = min(a.stages, ks1 - ks0);  // steps that need no free slot
+    int it = 0, ks = ks0;  // the producer's: stages and steps issued so far
     if (threadIdx.x == 0) {
         tma_prefetch_map(&mA0);
         tma_prefetch_map(&mB0);
@@ -133,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
         *abort_flag = 0;
         fence_mbar_init();
         chain_wait();
-        for (int s = 0; s < first; ++s) load_step(ks0 + s, s);
+        for (; it < a.stages && ks < ks1; ++it) ks += load_stage(ks, it);  // these need no free slot
     }
     if (warp == 1) {
         tmem_alloc(tmem_holder, a.tmem_cols);
@@ -149,12 +156,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         if (lane == 0) {
-            int s = first == a.stages ? 0 : first;
+            int s = 0;
             uint32_t ph = 0;
-            int it = first;
-            for (int ks = ks0 + first; ks < ks1; ++ks, ++it) {
+            for (; ks < ks1; ++it) {
                 if (!wait_or_abort(&empty[s], ph, abort_flag, a.flags)) break;
-                load_step(ks, s);
+                ks += load_stage(ks, s);
                 if (++s == a.stages) {
                     s = 0;
                     ph ^= 1;
@@ -173,16 +179,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
         const uint32_t stride = stage_bytes >> 4;
         int s = 0;
         uint32_t ph = 0, sum = 0;
-        for (int ks = ks0; ks < ks1; ++ks) {
+        for (int k = ks0, n; k < ks1; k += n) {
+            n = steps_of(k);
             if (!wait_or_abort_warp(&full[s], ph, abort_flag, a.flags)) break;
             tc_fence_after();
-            const uint64_t da = da0 + (uint32_t)s * stride, db = db0 + (uint32_t)s * stride;
+            uint64_t da = da0 + (uint32_t)s * stride, db = db0 + (uint32_t)s * stride;
+            for (int j = 0; j < n; ++j, da += step_bytes >> 4, db += step_bytes >> 4)
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-                mma_bf16_warp(tmem_base, da + kk * kStepA, db + kk * 2, idesc, sum);
-                if (kGated) mma_bf16_warp(tmem_base + a.tn, da + (kABytes >> 4) + kk * kStepA, db + kk * 2, idesc, sum);
-                sum = 1;
-            }
+                for (int kk = 0; kk < kBK / 16; ++kk) {
+                    mma_bf16_warp(tmem_base, da + kk * kStepA, db + kk * 2, idesc, sum);
+                    if (kGated) mma_bf16_warp(tmem_base + a.tn, da + (kABytes >> 4) + kk * kStepA, db + kk * 2, idesc, sum);
+                    sum = 1;
+                }
             mma_commit_warp(&empty[s]);
             if (++s == a.stages) {
                 s = 0;
@@ -360,7 +368,12 @@ void fill(Args& a, const Geometry& g, int64_t T, int N, int64_t k, int segs, boo
     a.steps = a.seg_steps * segs;
     a.tn = g.tn;
     a.splits = g.splits;
-    a.stages = std::min(kMaxStages, kRingBytes / (acc * kABytes + a.tn * kBK * 2));
+    const int step_bytes = acc * kABytes + a.tn * kBK * 2;
+    // two steps per stage halve the waits and commits between the MMAs (one token:
+    // 14336 -> 4096 20.7 instead of 21.8 us, 4096 -> 4096 8.8 instead of 9.7), but
+    // leave fewer stages: with three, 128 tokens, 7168 -> 2048 12.4 instead of 12.0
+    a.per = kRingBytes / (2 * step_bytes) >= (gated ? 3 : 4) ? 2 : 1;
+    a.stages = std::min(kMaxStages, kRingBytes / (a.per * step_bytes));
     const uint32_t cols = acc * a.tn;
     a.tmem_cols = 32;
     while (a.tmem_cols < cols) a.tmem_cols *= 2;
@@ -370,7 +383,7 @@ void fill(Args& a, const Geometry& g, int64_t T, int N, int64_t k, int segs, boo
 template <bool kGated, bool kAMN>
 cudaError_t launch(const CUtensorMap& A0, const CUtensorMap& A1, const CUtensorMap& B0, const CUtensorMap& B1,
                    const Args& a, const char* name, cudaStream_t st) {
-    auto* fn = dense_skinny_kernel<kGated, kAMN>;
+    auto* fn = a.per == 2 ? dense_skinny_kernel<kGated, kAMN, 2> : dense_skinny_kernel<kGated, kAMN, 1>;
     cudaError_t e = ensure_smem_attr(fn, kSmem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(cdiv(a.N, 128) * a.splits), (unsigned)cdiv(a.T, a.tn), 1);
