@@ -20,7 +20,7 @@
 // about 120 ns, and with one step per stage they were a fifth of the time.  TMEM
 // holds two accumulators, so a tile's epilogue overlaps the next tile's main
 // loop.  Bound by the tensor pipe and the power limit at large sizes (gate/up
-// forward, 4096 x 4096 -> 14336: 626 us in a short run, 1.54 PFLOP/s, the pipe 93%
+// forward, 4096 x 4096 -> 14336: 614 us in a short run, 1.57 PFLOP/s, the pipe 93%
 // active at 1.46 GHz), by the stores (weight gradients of few tokens) or the
 // operands' HBM reads otherwise.
 //

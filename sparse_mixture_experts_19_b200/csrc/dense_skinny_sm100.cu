@@ -45,6 +45,8 @@ constexpr int kABytes = 128 * kBK * 2;
 constexpr int kBox = 64 * kBK * 2;
 constexpr int kMaxStages = 12;
 constexpr int kRingBytes = 208 * 1024;
+// All of an SM's shared memory whatever the sizes: no second CTA that allocates TMEM
+// shares the SM, so an allocation never waits for a CTA whose cluster waits for this one.
 constexpr size_t kSmem = kRingBytes + 512 + 1024;
 constexpr int kRowBytes = 128 * 4;  // one token's 128 features, float32
 
