@@ -310,6 +310,13 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
+int step_bytes_of(int acc, int tn) { return acc * kABytes + tn * kBK * 2; }
+
+// Two steps per stage halve the waits and commits between the MMAs (one token:
+// 14336 -> 4096 20.7 instead of 21.8 us, 4096 -> 4096 8.8 instead of 9.7), but leave
+// fewer stages: with three, 128 tokens, 7168 -> 2048 12.4 instead of 12.0.
+int steps_per_stage(int acc, int tn) { return kRingBytes / (2 * step_bytes_of(acc, tn)) >= (acc == 2 ? 3 : 4) ? 2 : 1; }
+
 // One way of laying a product out, and its estimated time in microseconds.
 struct Geometry {
     int tn, splits;
@@ -326,8 +333,11 @@ struct Geometry {
 // that come from peers, and the tile's way out of TMEM and through the epilogue.
 // The weights come from HBM at 6.2 TB/s for one token tile, at 5.0 for several
 // (gate/up, 64 rows: 14336 -> 4096 takes 42.4 us in one tile and 52.3 in two, but
-// 2880 -> 2880, bound by its steps, 13.2 and 12.0).
-Geometry geometry(int64_t T, int N, int64_t k, int steps, int acc, int tn, int64_t most_ctas) {
+// 2880 -> 2880, bound by its steps, 13.2 and 12.0).  Issuing a step of a two-step
+// stage takes 0.20 us (192 rows, 2880 -> 2880: three tiles of 64, 10.0 us, not one of
+// 192, 11.7); for an input gradient, whose form is chosen together with the weight
+// gradient's, that figure moved backward passes by 20% both ways, and 0.29 stays.
+Geometry geometry(int64_t T, int N, int64_t k, int steps, int acc, int tn, int64_t most_ctas, bool fwd) {
     // clusters of s CTAs with 209 KB of shared memory each that a B200 holds at
     // once (a cluster stays inside a GPC), a little below what it reports
     static const int kFit[9] = {0, 148, 74, 44, 32, 26, 20, 0, 14};
@@ -338,8 +348,8 @@ Geometry geometry(int64_t T, int N, int64_t k, int steps, int acc, int tn, int64
     g.ctas = tiles * g.splits;
     const double rate = T <= tn ? 6.2e6 : 5.0e6;  // of the weights, read once or again by each token tile
     const double ctas = (double)g.ctas, rounds = (double)cdiv(g.ctas, 148), cols = tn * acc;
-    const double step =
-        std::max({0.29, 0.0016 * cols, (acc * kABytes + tn * kBK * 2) * std::min(ctas, 148.0) / 17.6e6});
+    const double issue = fwd && steps_per_stage(acc, tn) == 2 ? 0.20 : 0.29;
+    const double step = std::max({issue, 0.0016 * cols, step_bytes_of(acc, tn) * std::min(ctas, 148.0) / 17.6e6});
     const double stream = std::max(rounds * cdiv(steps, g.splits) * step, acc * (double)N * k * 2 / rate);
     g.us = 2.8 + stream + 0.016 * cols * (g.splits - 1) / g.splits + rounds * cols * (0.0094 + 0.017 / g.splits);
     return g;
@@ -349,14 +359,14 @@ Geometry geometry(int64_t T, int N, int64_t k, int steps, int acc, int tn, int64
 // accumulators) and down to 32, of at most most_ctas CTAs (tn = 0 when there is
 // none).
 constexpr int64_t kAnyCtas = INT64_MAX;
-Geometry best_geometry(int64_t T, int N, int64_t k, int segs, bool gated, int64_t most_ctas = kAnyCtas) {
+Geometry best_geometry(int64_t T, int N, int64_t k, int segs, bool gated, int64_t most_ctas, bool fwd) {
     const int acc = gated ? 2 : 1, steps = cdiv(k, kBK) * segs;
     const int64_t least = cdiv(T, 256 / acc);
     Geometry best{};
     for (int64_t n = least; n < least + 8; ++n) {
         const int tn = cdiv(cdiv(T, n), 16) * 16;
         if (n > least && tn < 32) break;
-        const Geometry g = geometry(T, N, k * segs, steps, acc, tn, most_ctas);
+        const Geometry g = geometry(T, N, k * segs, steps, acc, tn, most_ctas, fwd);
         if (g.ctas <= most_ctas && (best.tn == 0 || g.us < best.us)) best = g;
     }
     return best;
@@ -370,12 +380,8 @@ void fill(Args& a, const Geometry& g, int64_t T, int N, int64_t k, int segs, boo
     a.steps = a.seg_steps * segs;
     a.tn = g.tn;
     a.splits = g.splits;
-    const int step_bytes = acc * kABytes + a.tn * kBK * 2;
-    // two steps per stage halve the waits and commits between the MMAs (one token:
-    // 14336 -> 4096 20.7 instead of 21.8 us, 4096 -> 4096 8.8 instead of 9.7), but
-    // leave fewer stages: with three, 128 tokens, 7168 -> 2048 12.4 instead of 12.0
-    a.per = kRingBytes / (2 * step_bytes) >= (gated ? 3 : 4) ? 2 : 1;
-    a.stages = std::min(kMaxStages, kRingBytes / (a.per * step_bytes));
+    a.per = steps_per_stage(acc, a.tn);
+    a.stages = std::min(kMaxStages, kRingBytes / (a.per * step_bytes_of(acc, a.tn)));
     const uint32_t cols = acc * a.tn;
     a.tmem_cols = 32;
     while (a.tmem_cols < cols) a.tmem_cols *= 2;
@@ -446,21 +452,21 @@ struct Choice {
     double us;
 };
 
-// The form whose estimated time is less.  At T = 128 the few-row form takes 9.7
+// The form whose estimated time is less.  At T = 128 the few-row form takes 9.0
 // against 14.9 us on 2880 -> 2880 (pairs: 23 tiles for 74 pairs); at T = 256 it
 // takes 42.8 against 33.5 us on 4096 -> 14336, where 112 feature tiles read the
 // tokens 112 times.
 Choice choose(int64_t T, int N, int64_t k, int segs, bool gated, double pair_steps, int pair_ctas,
-              int64_t most_ctas = kAnyCtas) {
+              int64_t most_ctas = kAnyCtas, bool fwd = false) {
     Choice c{false, {}, pair_ctas, pairs_us(T, N, k, segs, gated, pair_steps)};
     if (T > 65535 * 16) return c;  // the grid's second dimension counts token tiles
-    const Geometry g = best_geometry(T, N, k, segs, gated, most_ctas);
+    const Geometry g = best_geometry(T, N, k, segs, gated, most_ctas, fwd);
     if (g.tn && (g.us < c.us || c.ctas > most_ctas)) c = Choice{true, g, g.ctas, g.us};
     return c;
 }
 
 Choice choose_fwd(int64_t T, int K, int N, bool gated) {
-    return choose(T, N, K, 1, gated, dense_fwd_pairs_steps(T, K, N, gated), 0);
+    return choose(T, N, K, 1, gated, dense_fwd_pairs_steps(T, K, N, gated), 0, kAnyCtas, true);
 }
 
 // The input gradient's form, and how the weight gradient (where one follows)
