@@ -183,14 +183,20 @@ def _stream(stream):
 
 def _on(stream):
     """Makes `stream` current for a convenience form's own allocations and
-    fills, so that they are ordered with the kernels it enqueues."""
+    fills, so that they are ordered with the kernels it enqueues.  A torch
+    stream, a raw handle, or an object that has one as `cuda_stream`."""
     import contextlib
 
     import torch
 
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        # 0 and 1 are the default stream's handles (none, cudaStreamLegacy); as an
+        # external stream's, 0 would mean "none given": a stream of torch's own
+        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+    return torch.cuda.stream(stream)
 
 
 def workspace(cfg: moe_config_t, device="cuda"):

@@ -1,0 +1,79 @@
+"""The operators around the routed layer on the GPU: raw stream handles, rings
+and split tiles that are used again and again, the forms a product takes, far
+activations and the largest sizes.  References are the formulas in float64;
+the tolerances are those of test_block_ops.py, from which the checks come, and
+what a test adds is derived where it stands."""
+import pytest
+import torch
+
+from test_block_ops import (ACTS, BF, F32, U8, U24, acc_tol, act64, canary_intact, gen_of, guarded, norm64, rnd,
+                            test_gated_backward as check_gated_backward, test_gated_forward as check_gated_forward,
+                            test_linear_backward as check_linear_backward,
+                            test_linear_forward as check_linear_forward, within)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------- streams
+class Handle:
+    """A stream object of another library: a handle, nothing else."""
+
+    def __init__(self, cuda_stream):
+        self.cuda_stream = cuda_stream
+
+
+def block_operands(g, T=70, H=256, I=128, E=8):
+    x, dy, rw = rnd(g, T, H), rnd(g, T, H), rnd(g, E, H, scale=H ** -0.5)
+    nw = rnd(g, H, scale=0.1, dtype=F32, shift=1.0)
+    wg, wu, wd = rnd(g, I, H, scale=H ** -0.5), rnd(g, I, H, scale=H ** -0.5), rnd(g, H, I, scale=I ** -0.5)
+    return x, dy, rw, nw, wg, wu, wd
+
+
+@pytest.mark.parametrize("handle", [0, 1, Handle(0)])
+def test_default_stream_by_its_handle(gpu_lib, handle):
+    """stream=0 is the default stream: a call there from within another stream
+    waits for an input that the default stream writes late."""
+    moe = gpu_lib
+    x, dy, rw, nw, wg, wu, wd = block_operands(gen_of(21))
+    ew = [w.unsqueeze(0).repeat(8, 1, 1) for w in (wg, wu, wd)]
+    late, late_dy = torch.empty_like(x), torch.empty_like(dy)
+
+    def calls(x, dy, stream):
+        y, kept = moe.ffn_block(x, nw, wg, wu, wd, keep=True, stream=stream)
+        return [moe.forward(x, rw, *ew, 2, stream=stream), moe.norm(x, nw, stream=stream),
+                moe.linear(x, wg, stream=stream), moe.gated(x, wg, wu, stream=stream), y,
+                *(t for t in moe.ffn_block_backward(dy, kept, stream=stream).values() if t is not None)]
+
+    want = calls(x, dy, None)
+    late.zero_()
+    late_dy.zero_()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(100_000_000)  # about 60 ms of the default stream
+    late.copy_(x)
+    late_dy.copy_(dy)
+    with torch.cuda.stream(side):
+        got = calls(late, late_dy, handle)
+    torch.cuda.default_stream().synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_stream_handles_of_torch_streams(gpu_lib):
+    """A torch stream, its handle and an object that holds the handle are one
+    stream; 2 (the calling thread's default stream) is passed on."""
+    moe = gpu_lib
+    st = torch.cuda.Stream()
+    for s in (st, st.cuda_stream, Handle(st.cuda_stream)):
+        with moe._on(s):
+            assert torch.cuda.current_stream().cuda_stream == st.cuda_stream
+    with torch.cuda.stream(st), moe._on(0):
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    with moe._on(2):
+        assert torch.cuda.current_stream().cuda_stream == 2
+    g = gen_of(22)
+    x, w = rnd(g, 40, 64), rnd(g, 72, 64)
+    want = moe.linear(x, w)
+    torch.cuda.synchronize()
+    y = moe.linear(x, w, stream=2)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
