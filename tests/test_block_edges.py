@@ -3,6 +3,8 @@ and split tiles that are used again and again, the forms a product takes, far
 activations and the largest sizes.  References are the formulas in float64;
 the tolerances are those of test_block_ops.py, from which the checks come, and
 what a test adds is derived where it stands."""
+import math
+
 import pytest
 import torch
 
@@ -77,3 +79,25 @@ def test_stream_handles_of_torch_streams(gpu_lib):
     y = moe.linear(x, w, stream=2)
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+# ------------------------------------------------- activations, far tails
+def test_gelu_lower_tail(gpu_lib):
+    """GELU and its slope keep their relative accuracy where both fall off to
+    zero: one rounding to bf16 (of the slope as an operand; dx repeats it), and
+    2^-13 for the function: 5.6e-5 for the polynomial, 1.6e-5 for the exponential,
+    whose argument is at most 122 and off by 3 * 2^-24 of itself (times ln 2), and
+    a few 1e-7 for the special function unit.  The slope's terms cancel by
+    1 / (z^2 - 1): below -3 that at most doubles their error."""
+    moe = gpu_lib
+    z = torch.linspace(-12.75, -3.0, 1280, device="cuda").to(BF).view(160, 8)
+    eye = torch.eye(8, device="cuda").to(BF)
+    z64 = z.double()
+    cdf = torch.special.erfc(-z64 / math.sqrt(2)) / 2  # torch's ndtr is 0 below about -6 on this device
+    val, slope = z64 * cdf, cdf + z64 * torch.exp(-z64 * z64 / 2) / math.sqrt(2 * math.pi)
+    within(moe.linear(z, eye, act="gelu"), val, (U8 + (1 + U8) * 2.0 ** -13) * val.abs(), "gelu")
+    h = moe.gated(z, eye, torch.zeros_like(eye), b_up=torch.ones(8, device="cuda"), act="gelu")
+    within(h, val, (U8 + (1 + U8) * 2.0 ** -13) * val.abs(), "gated gelu")
+    cfg, dx = moe.dense_config(160, 8, 8, "gelu"), torch.empty_like(z)
+    moe.moe_linear_backward(cfg, torch.ones_like(z), z, eye, z, dx, None, None, moe.linear_backward_workspace(cfg))
+    within(dx, slope, (U8 + (1 + U8) * 2.0 ** -12) * slope.abs(), "slope")
