@@ -710,7 +710,10 @@ Args args_of(const Problem& pr, const DenseWs& ws) {
     a.N = pr.N;
     a.mt = cdiv(pr.M, 2 * kBM);
     a.nt = cdiv(pr.N, pr.bn);
-    a.gm = band_of((int64_t)pr.seg_steps * pr.segs * kBK);
+    // no more than there are, so that a band's tiles, gm x nt, are no more than all of
+    // them: 1024 row tiles of 2^22 column tiles (one row of 2^30 outputs) would not
+    // fit an int
+    a.gm = std::min(a.mt, band_of((int64_t)pr.seg_steps * pr.segs * kBK));
     a.seg_steps = pr.seg_steps;
     a.steps = pr.seg_steps * pr.segs;
     a.full = p.full;

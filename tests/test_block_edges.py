@@ -101,3 +101,30 @@ def test_gelu_lower_tail(gpu_lib):
     cfg, dx = moe.dense_config(160, 8, 8, "gelu"), torch.empty_like(z)
     moe.moe_linear_backward(cfg, torch.ones_like(z), z, eye, z, dx, None, None, moe.linear_backward_workspace(cfg))
     within(dx, slope, (U8 + (1 + U8) * 2.0 ** -12) * slope.abs(), "slope")
+
+
+# --------------------------------------------------------- largest sizes
+def test_more_than_two_to_the_30_columns(gpu_lib):
+    """One row, 2^30 + 264 outputs (or inputs) of eight: every column."""
+    moe, g = gpu_lib, gen_of(23)
+    W, step = 2 ** 30 + 264, 2 ** 26
+    w = torch.empty((W, 8), dtype=BF, device="cuda").normal_(generator=g)
+    x = rnd(g, 1, 8)
+    y = moe.linear(x, w)
+    for c in range(0, W, step):
+        v = w[c:c + step].double()
+        ref, size = v @ x[0].double(), v.abs() @ x[0].double().abs()
+        within(y[0, c:c + step], ref, U8 * ref.abs() + (1 + U8) * acc_tol(8) * size, f"y from {c}")
+    del y
+    w = w.view(8, W)
+    x, dy = rnd(g, 1, W), rnd(g, 1, 8)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    cfg = moe.dense_config(1, W, 8, grad_dtype="bf16")
+    ws = moe.linear_backward_workspace(cfg)
+    moe.moe_linear_backward(cfg, dy, x, w, None, dx, dw, None, ws)
+    for c in range(0, W, step):
+        v = w[:, c:c + step].double()
+        ref, size = dy[0].double() @ v, dy[0].double().abs() @ v.abs()
+        within(dx[0, c:c + step], ref, U8 * ref.abs() + (1 + U8) * acc_tol(8) * size, f"dx from {c}")
+        assert torch.equal(dw[:, c:c + step], (dy.float().t() * x[:, c:c + step].float()).to(BF)), f"d_w from {c}"
+    assert moe.moe_dense_get_device_status(ws) == 0
