@@ -204,19 +204,21 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
     } else if (warp < 10) {
         // ------------------------------------------------ TMEM -> part[accumulator][token][128 features]
         // (in the ring's place: the accumulator is complete, so every step's
-        // operands have been read)
+        // operands have been read; after a time-out it may not be, and copies may
+        // still be landing: then nothing is moved, and the device flag tells of y)
         const int q = warp & 3, half = (warp - 2) >> 2;  // lanes, every second group of 16 columns
-        wait_sleep_or_abort(done, 0, abort_flag, a.flags);
-        tc_fence_after();
-        float* part = reinterpret_cast<float*>(smem);
+        if (wait_sleep_or_abort_warp(done, 0, abort_flag, a.flags)) {
+            tc_fence_after();
+            float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int p = 0; p < kAcc; ++p)
-            for (int c = 16 * half; c < tokens; c += 32) {
-                float v[16];
-                tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + p * a.tn + c, v);
+            for (int p = 0; p < kAcc; ++p)
+                for (int c = 16 * half; c < tokens; c += 32) {
+                    float v[16];
+                    tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + p * a.tn + c, v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) part[(p * a.tn + c + i) * 128 + q * 32 + lane] = v[i];
-            }
+                    for (int i = 0; i < 16; ++i) part[(p * a.tn + c + i) * 128 + q * 32 + lane] = v[i];
+                }
+        }
         tc_fence_before();
     }
     __syncwarp();  // the single-lane roles join their warps

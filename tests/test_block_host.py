@@ -1,9 +1,12 @@
 """The operators around the routed layer, host side: what needs no GPU."""
+import os
+import re
 import types
 
 import pytest
 
 import sparse_mixture_experts_19_b200 as moe
+from sparse_mixture_experts_19_b200 import build
 
 
 # ------------------------------------------------------------- streams
@@ -24,3 +27,15 @@ def test_raw_stream_handles(streams, stream, want):
     """Handle 0 is the default stream, in a call of the convenience forms too,
     and an object needs no more than its handle."""
     assert moe._on(stream) == ("on", want)
+
+
+# --------------------------------------------------- waits of whole warps
+@pytest.mark.parametrize("name", ["dense_gemm_sm100.cu", "dense_skinny_sm100.cu"])
+def test_collective_waits(name):
+    """In the dense kernels only the producer's single lane waits by itself; a
+    warp whose next instruction takes all of its lanes (tcgen05.ld among them)
+    waits in the form that gives each lane the same answer, and looks at it."""
+    code = [line.split("//")[0] for line in open(os.path.join(build.CSRC, name))]
+    waits = [line.strip() for line in code if re.search(r"\b(wait_or_abort|wait_sleep_or_abort)(_warp)?\(", line)]
+    assert len([w for w in waits if "_warp(" not in w]) == 1 and len(waits) >= 3
+    assert all(re.match(r"if \(!?wait_", w) for w in waits), waits
