@@ -468,7 +468,8 @@ moe_status_t moe_backward(const moe_config_t* cfg, const void* x, const void* dy
  *     the same values gives the same bits (no sum depends on timing; which
  *     outputs a backward call is asked for may choose the order of summation);
  *   - a tensor the call writes must not overlap another one of the call,
- *     except where stated;
+ *     except where stated (the two are then the same tensor), and none may
+ *     overlap the workspace: MOE_ERR_INVALID_ARG;
  *   - NaN and infinity propagate as the formulas have them.
  */
 typedef enum {
@@ -509,8 +510,8 @@ moe_status_t moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const
  *   dy [T, H] in dy_dtype; x, weight as in the forward; mean (NULL for
  *   MOE_NORM_RMS), rstd [T] as the forward wrote them; d_residual [T, H] or
  *   NULL: the gradient that reaches x past the norm; d_weight, d_bias [H]
- *   float32 or NULL to skip.  dx may be d_residual, or dy when both have the
- *   same type.  ws: moe_norm_workspace_size(cfg) bytes, 256-byte aligned
+ *   float32 or NULL to skip.  dx may be d_residual or x, or dy when both have
+ *   the same type.  ws: moe_norm_workspace_size(cfg) bytes, 256-byte aligned
  *   (partial sums, behind MOE_DENSE_WS_HEADER bytes that are left alone).
  */
 size_t moe_norm_workspace_size(const moe_norm_config_t* cfg);

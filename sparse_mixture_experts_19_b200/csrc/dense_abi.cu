@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "abi_util.cuh"
 #include "dense.cuh"
@@ -105,16 +106,57 @@ size_t grad_bytes(const moe_dense_config_t* c) {
     return (size_t)c->N * c->K * (c->grad_dtype == MOE_F32 ? 4 : 2);
 }
 
+// A tensor of a call: n bytes at p (null: not given).  in_place: an input that
+// the first output may replace.
+struct Span {
+    const char* name;
+    const void* p;
+    size_t n;
+    bool in_place = false;
+    bool meets(const Span& o) const {
+        const uintptr_t a = (uintptr_t)p, b = (uintptr_t)o.p;
+        return p && o.p && n && o.n && a < b + o.n && b < a + n;
+    }
+};
+
+moe_status_t shared(const Span& a, const Span& b) {
+    return a.p == b.p ? fail(MOE_ERR_INVALID_ARG, "%s and %s are the same tensor", a.name, b.name)
+                      : fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+}
+
+// Refuses an output that shares bytes with another tensor of the call, and a
+// workspace that shares bytes with any.
+moe_status_t check_apart(std::initializer_list<Span> out, std::initializer_list<Span> in, const Span& ws = {}) {
+    for (const Span* o = out.begin(); o != out.end(); ++o) {
+        for (const Span& i : in)
+            if (o->meets(i) && !(i.in_place && o == out.begin() && o->p == i.p && o->n == i.n)) return shared(*o, i);
+        for (const Span* q = o + 1; q != out.end(); ++q)
+            if (o->meets(*q)) return shared(*q, *o);
+    }
+    for (auto list : {out, in})
+        for (const Span& t : list)
+            if (t.meets(ws)) return shared(t, ws);
+    return MOE_OK;
+}
+
+size_t f32s(int64_t n) { return (size_t)n * sizeof(float); }
+
+// Bytes of a dense call's tensors: bf16 [T, K], [T, N], [N, K]; float32 [N]; a
+// weight gradient.
+struct DenseBytes {
+    size_t tk, tn, nk, n, dw;
+    explicit DenseBytes(const moe_dense_config_t* c)
+        : tk((size_t)c->T * c->K * 2),
+          tn((size_t)c->T * c->N * 2),
+          nk((size_t)c->N * c->K * 2),
+          n(f32s(c->N)),
+          dw(grad_bytes(c)) {}
+};
+
 }  // namespace
 }  // namespace moe
 
 using namespace moe;
-
-#define NOT_SAME(a, b)                                                                          \
-    do {                                                                                        \
-        if ((a) && (const void*)(a) == (const void*)(b))                                        \
-            return fail(MOE_ERR_INVALID_ARG, "%s and %s are the same tensor", #a, #b);          \
-    } while (0)
 
 extern "C" {
 
@@ -130,6 +172,10 @@ moe_status_t moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const
     OPTIONAL_PTR(bias);
     OPTIONAL_PTR(mean_out);
     OPTIONAL_PTR(rstd_out);
+    const size_t es = cfg->dtype == MOE_F32 ? 4 : 2, rows = (size_t)cfg->T * cfg->H * es;
+    s = check_apart({{"y", y, rows}, {"mean_out", mean_out, f32s(cfg->T)}, {"rstd_out", rstd_out, f32s(cfg->T)}},
+                    {{"x", x, rows, true}, {"weight", weight, f32s(cfg->H)}, {"bias", bias, f32s(cfg->H)}});
+    if (s != MOE_OK) return s;
     if (cfg->T == 0) return MOE_OK;
     REQUIRE_PTR(x);
     REQUIRE_PTR(y);
@@ -161,6 +207,16 @@ moe_status_t moe_norm_backward(const moe_norm_config_t* cfg, const void* dy, con
     OPTIONAL_PTR(d_residual);
     OPTIONAL_PTR(d_weight);
     OPTIONAL_PTR(d_bias);
+    const size_t n = (size_t)cfg->T * cfg->H, rows = n * (cfg->dtype == MOE_F32 ? 4 : 2);
+    s = check_apart({{"dx", dx, rows}, {"d_weight", d_weight, f32s(cfg->H)}, {"d_bias", d_bias, f32s(cfg->H)}},
+                    {{"dy", dy, n * (cfg->dy_dtype == MOE_F32 ? 4 : 2), true},
+                     {"x", x, rows, true},
+                     {"d_residual", d_residual, rows, true},
+                     {"weight", weight, f32s(cfg->H)},
+                     {"mean", mean, f32s(cfg->T)},
+                     {"rstd", rstd, f32s(cfg->T)}},
+                    {"ws", ws, norm_ws_bytes(cfg)});
+    if (s != MOE_OK) return s;
     cudaStream_t st = (cudaStream_t)stream;
     if (cfg->T == 0) {
         if (d_weight) CUDA_TRY(cudaMemsetAsync(d_weight, 0, sizeof(float) * cfg->H, st), "memset");
@@ -172,7 +228,6 @@ moe_status_t moe_norm_backward(const moe_norm_config_t* cfg, const void* dy, con
     if (cfg->kind == MOE_NORM_LAYER) REQUIRE_PTR(mean);
     REQUIRE_PTR(rstd);
     REQUIRE_PTR(dx);
-    if (cfg->dy_dtype != cfg->dtype) NOT_SAME(dx, dy);
     NormArgs a{};
     a.T = cfg->T;
     a.H = cfg->H;
@@ -210,10 +265,11 @@ moe_status_t moe_linear_forward(const moe_dense_config_t* cfg, const void* x, co
     OPTIONAL_PTR(residual);
     REQUIRE_PTR(y);
     OPTIONAL_PTR(z_out);
-    NOT_SAME(y, x);
-    NOT_SAME(z_out, x);
-    NOT_SAME(z_out, y);
-    NOT_SAME(z_out, residual);
+    const DenseBytes b(cfg);
+    s = check_apart({{"y", y, b.tn}, {"z_out", z_out, b.tn}},
+                    {{"x", x, b.tk}, {"w", w, b.nk}, {"bias", bias, b.n}, {"residual", residual, b.tn, true}},
+                    {"ws", ws, p.bytes});
+    if (s != MOE_OK) return s;
     DenseOut o{};
     o.act = cfg->act;
     o.bias0 = bias;
@@ -233,6 +289,10 @@ moe_status_t moe_linear_backward(const moe_dense_config_t* cfg, const void* dy, 
     OPTIONAL_PTR(dx);
     OPTIONAL_PTR(d_w);
     OPTIONAL_PTR(d_bias);
+    const DenseBytes b(cfg);
+    s = check_apart({{"dx", dx, b.tk}, {"d_w", d_w, b.dw}, {"d_bias", d_bias, b.n}},
+                    {{"dy", dy, b.tn}, {"x", x, b.tk}, {"w", w, b.nk}, {"z", z, b.tn}}, {"ws", ws, p.bytes});
+    if (s != MOE_OK) return s;
     cudaStream_t st = (cudaStream_t)stream;
     if (cfg->T == 0) {
         if (d_w) CUDA_TRY(cudaMemsetAsync(d_w, 0, grad_bytes(cfg), st), "memset");
@@ -244,12 +304,6 @@ moe_status_t moe_linear_backward(const moe_dense_config_t* cfg, const void* dy, 
     if (d_w) REQUIRE_PTR(x);
     if (dx) REQUIRE_PTR(w);
     if (act) REQUIRE_PTR(z);
-    NOT_SAME(dx, dy);
-    NOT_SAME(dx, x);
-    NOT_SAME(dx, w);
-    NOT_SAME(d_w, x);
-    NOT_SAME(d_w, w);
-    NOT_SAME(d_w, dx);
     const bf16* dz = act ? p.dz0 : (const bf16*)dy;
     if (d_bias || (act && (dx || d_w))) {
         DenseDzArgs a{};
@@ -288,12 +342,12 @@ moe_status_t moe_gated_forward(const moe_dense_config_t* cfg, const void* x, con
     REQUIRE_PTR(h);
     OPTIONAL_PTR(g_out);
     OPTIONAL_PTR(u_out);
-    NOT_SAME(h, x);
-    NOT_SAME(g_out, h);
-    NOT_SAME(u_out, h);
-    NOT_SAME(g_out, u_out);
-    NOT_SAME(g_out, x);
-    NOT_SAME(u_out, x);
+    const DenseBytes b(cfg);
+    s = check_apart({{"h", h, b.tn}, {"g_out", g_out, b.tn}, {"u_out", u_out, b.tn}},
+                    {{"x", x, b.tk}, {"w_gate", w_gate, b.nk}, {"w_up", w_up, b.nk}, {"b_gate", b_gate, b.n},
+                     {"b_up", b_up, b.n}},
+                    {"ws", ws, p.bytes});
+    if (s != MOE_OK) return s;
     DenseOut o{};
     o.act = cfg->act;
     o.bias0 = b_gate;
@@ -318,7 +372,13 @@ moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, c
     OPTIONAL_PTR(d_b_gate);
     OPTIONAL_PTR(d_b_up);
     if (!d_w_gate != !d_w_up) return fail(MOE_ERR_INVALID_ARG, "d_w_gate and d_w_up go together");
-    NOT_SAME(d_w_gate, d_w_up);
+    const DenseBytes b(cfg);
+    s = check_apart({{"dx", dx, b.tk}, {"d_w_gate", d_w_gate, b.dw}, {"d_w_up", d_w_up, b.dw}, {"d_b_gate", d_b_gate, b.n},
+                     {"d_b_up", d_b_up, b.n}},
+                    {{"dh", dh, b.tn}, {"x", x, b.tk}, {"w_gate", w_gate, b.nk}, {"w_up", w_up, b.nk}, {"g", g, b.tn},
+                     {"u", u, b.tn}},
+                    {"ws", ws, p.bytes});
+    if (s != MOE_OK) return s;
     cudaStream_t st = (cudaStream_t)stream;
     if (cfg->T == 0) {
         if (d_w_gate) CUDA_TRY(cudaMemsetAsync(d_w_gate, 0, grad_bytes(cfg), st), "memset");
@@ -334,15 +394,6 @@ moe_status_t moe_gated_backward(const moe_dense_config_t* cfg, const void* dh, c
     if (dx) {
         REQUIRE_PTR(w_gate);
         REQUIRE_PTR(w_up);
-    }
-    NOT_SAME(dx, x);
-    NOT_SAME(dx, w_gate);
-    NOT_SAME(dx, w_up);
-    for (const void* d_w : {d_w_gate, d_w_up}) {
-        NOT_SAME(d_w, x);
-        NOT_SAME(d_w, w_gate);
-        NOT_SAME(d_w, w_up);
-        NOT_SAME(d_w, dx);
     }
     DenseDzArgs a{};
     a.T = cfg->T;

@@ -128,3 +128,49 @@ def test_more_than_two_to_the_30_columns(gpu_lib):
         within(dx[0, c:c + step], ref, U8 * ref.abs() + (1 + U8) * acc_tol(8) * size, f"dx from {c}")
         assert torch.equal(dw[:, c:c + step], (dy.float().t() * x[:, c:c + step].float()).to(BF)), f"d_w from {c}"
     assert moe.moe_dense_get_device_status(ws) == 0
+
+
+# ------------------------------------------------------------ neighbours
+def test_neighbours_and_in_place(gpu_lib):
+    """Tensors that touch, end to start, are not an overlap; the norm's dx in
+    place of x, of dy and of d_residual."""
+    moe, g = gpu_lib, gen_of(24)
+    T, K, N = 24, 64, 40
+
+    def packed(*shapes, dtype=BF):
+        sizes = [math.prod(s) for s in shapes]
+        return [t.view(s) for t, s in zip(torch.empty(sum(sizes), dtype=dtype, device="cuda").split(sizes), shapes)]
+
+    x, w, wu, res, y, z, u, dx, dw, dwu = packed((T, K), (N, K), (N, K), (T, N), (T, N), (T, N), (T, N), (T, K), (N, K),
+                                                 (N, K))
+    b, db, dbu = packed((N,), (N,), (N,), dtype=F32)
+    for t in (x, w, wu, res, b):
+        t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+    cfg = moe.dense_config(T, K, N, "silu", grad_dtype="bf16")
+    ws = moe._new_ws(max(moe.moe_gated_backward_workspace_size(cfg), moe.moe_linear_workspace_size(cfg)), "cuda")
+    moe.moe_linear_forward(cfg, x, w, b, res, y, z, ws)
+    assert torch.equal(y, moe.linear(x.clone(), w.clone(), b.clone(), res.clone(), "silu"))
+    moe.moe_gated_forward(cfg, x, w, wu, b, None, y, z, u, ws)
+    assert torch.equal(y, moe.gated(x.clone(), w.clone(), wu.clone(), b.clone()))
+    moe.moe_gated_backward(cfg, res, x, w, wu, z, u, dx, dw, dwu, db, dbu, ws)
+    own = [torch.empty_like(t) for t in (dx, dw, dwu, db, dbu)]
+    moe.moe_gated_backward(cfg, res.clone(), x.clone(), w.clone(), wu.clone(), z.clone(), u.clone(), *own,
+                           moe.gated_backward_workspace(cfg))
+    assert all(torch.equal(p, q) for p, q in zip((dx, dw, dwu, db, dbu), own))
+    # rows of every ring form: one warp and several, two rows and one kept
+    for T, H, dt in ((700, 264, BF), (700, 4104, BF), (300, 8200, F32), (200, 16384, F32)):
+        x, dy, dr = (rnd(g, T, H, dtype=dt) for _ in range(3))
+        mean, rstd = (torch.empty(T, device="cuda") for _ in range(2))
+        moe.norm(x, mean_out=mean, rstd_out=rstd)
+        cfg = moe.norm_config(T, H, dtype="bf16" if dt == BF else "f32")
+        ws = moe.norm_workspace(cfg)
+
+        def grads(x, dy, dr, dx):
+            dw, db = (torch.empty(H, device="cuda") for _ in range(2))
+            moe.moe_norm_backward(cfg, dy, x, None, mean, rstd, dr, dx, dw, db, ws)
+            return dx, dw, db
+
+        want = grads(x, dy, dr, torch.empty_like(x))
+        for i in range(3):
+            a = [x.clone(), dy.clone(), dr.clone()]
+            assert all(torch.equal(p, q) for p, q in zip(grads(*a, a[i]), want)), (H, i)
