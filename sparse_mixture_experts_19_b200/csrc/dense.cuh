@@ -73,9 +73,11 @@ struct DenseOut {
 struct DenseWs {
     int32_t* flags;
     uint32_t* counters;  // zero between calls
+    uint32_t* gate;      // two words, zero between calls: the backward products' (sm100_dense.cuh)
     float* part;         // the product's ..._part_floats
 };
-constexpr size_t kDenseCounterBytes = 4864;  // of one product
+constexpr size_t kDenseCounterBytes = 4864;  // of one product, and the gate
+constexpr size_t kDenseGateOffset = kDenseCounterBytes - 128;
 
 // y = act(x W^T + b) + res; gated (w1 non-null): y = act(x W0^T + b0) (x W1^T + b1).
 size_t dense_fwd_part_floats(int64_t T, int K, int N, bool gated);

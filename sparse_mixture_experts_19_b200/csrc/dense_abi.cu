@@ -68,7 +68,9 @@ void make_dense_plan(const moe_dense_config_t* c, bool gated, bool backward, voi
     *p = DensePlan{};
     p->ws.flags = (int32_t*)take(64);
     p->ws.counters = (uint32_t*)take(kDenseCounterBytes);
+    if (base) p->ws.gate = p->ws.counters + kDenseGateOffset / sizeof(uint32_t);
     p->wws.flags = p->ws.flags;
+    p->wws.gate = p->ws.gate;
     const int two = gated ? 2 : 1;
     if (backward && c->T > 0) {
         const size_t tn = (size_t)c->T * c->N;

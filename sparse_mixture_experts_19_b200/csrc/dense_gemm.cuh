@@ -24,7 +24,8 @@ size_t dense_fwd_pairs_part_floats(int64_t T, int K, int N, bool gated);
 size_t dense_dgrad_pairs_part_floats(int64_t T, int K, int N, int segs);
 cudaError_t launch_dense_fwd_pairs(const void* x, const void* w0, const void* w1, int64_t T, int K, int N,
                                    const DenseOut& o, const DenseWs& ws, cudaStream_t st);
+// opens_gate: for a weight gradient that starts beside this kernel.
 cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T,
-                                     int K, int N, void* dx, const DenseWs& ws, cudaStream_t st);
+                                     int K, int N, void* dx, bool opens_gate, const DenseWs& ws, cudaStream_t st);
 
 }  // namespace moe

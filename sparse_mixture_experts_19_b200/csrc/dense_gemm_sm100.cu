@@ -101,7 +101,8 @@ struct Args {
     bool has_res, has_z0, has_z1;
     float* part;         // partial sums of the split tiles
     uint32_t* counters;  // [split tiles][2 CTAs][8 warps]; null: sum_units_kernel adds the splits
-    bool late_wait;      // the kernel before this one writes nothing that this one uses
+    bool late_wait;      // the kernel before this one writes nothing that this one uses, and opens the gate
+    uint32_t* gate;      // to wait at (late_wait) or to open, or null
     int32_t* flags;
 };
 
@@ -234,17 +235,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_g
         tmem_alloc_pair(tmem_holder, kTmemCols);
         tmem_relinquish_pair();
     }
+    // beside the kernel before this one: the operands, from who has waited for them
+    bool shut = false;
+    if (a.late_wait && threadIdx.x == kThreads - 1) shut = !gate_wait(a.gate);
+    __syncwarp();
     tc_fence_before();
     cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    if (!a.late_wait) chain_wait();
+    if (!a.late_wait) {
+        chain_wait();
+        if (a.gate && blockIdx.x == 0 && threadIdx.x == kThreads - 1) gate_open(a.gate);
+    } else if (threadIdx.x == kThreads - 1) {
+        if (shut) {
+            *abort_flag = 1;
+            atomicOr(a.flags, 0x2);
+        } else {
+            gate_passed(a.gate);
+        }
+    }
     chain_next();
     const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer (both CTAs)
         if (lane == 0) {
+            if (a.late_wait) fence_async_global();
             uint32_t it = 0;
             for (int t = pair; t < a.total && !*abort_flag; t += npairs) {
                 const Tile ti = decode<kBN>(t, a);
@@ -669,7 +685,7 @@ TailPlan tail_plan(int64_t tiles, int steps, Split how) {
 
 constexpr int64_t kUnitFloats = 256 * 256;
 constexpr size_t kCounterBytes = (size_t)kDensePairs * 2 * kEpiWarps * sizeof(uint32_t);
-static_assert(kCounterBytes <= kDenseCounterBytes, "counters");
+static_assert(kCounterBytes <= kDenseGateOffset, "counters");
 
 // Time of a tile of 128 columns against one of 256.
 constexpr double kNarrow = 0.65;
@@ -783,7 +799,7 @@ cudaError_t launch_dense_fwd_pairs(const void* x, const void* w0, const void* w1
 }
 
 cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const void* w0, const void* w1, int64_t T,
-                                     int K, int N, void* dx, const DenseWs& ws, cudaStream_t st) {
+                                     int K, int N, void* dx, bool opens_gate, const DenseWs& ws, cudaStream_t st) {
     Maps m;
     bool ok = make_tile_map(&m.A0, false, dz0, N, T, 1, kBM) && make_tile_map(&m.B0, false, w0, K, N, 1, 64) &&
               make_tile_map(&m.D0, false, dx, K, T, 1, 32);
@@ -793,7 +809,8 @@ cudaError_t launch_dense_dgrad_pairs(const void* dz0, const void* dz1, const voi
     if (dz1)
         ok = ok && make_tile_map(&m.A1, false, dz1, N, T, 1, kBM) && make_tile_map(&m.B1, false, w1, K, N, 1, 64);
     if (!ok) return cudaErrorInvalidValue;
-    const Args a = args_of(dgrad_problem(T, K, N, dz1 ? 2 : 1), ws);
+    Args a = args_of(dgrad_problem(T, K, N, dz1 ? 2 : 1), ws);
+    a.gate = opens_gate ? ws.gate : nullptr;
     return launch<kPlain, false, true, 256>(m, a, dz1 ? "gated_dgrad" : "linear_dgrad", st);
 }
 
@@ -809,6 +826,7 @@ cudaError_t launch_dense_wgrad(const void* dz0, const void* dz1, const void* x, 
     if (!ok) return cudaErrorInvalidValue;
     Args a = args_of(wgrad_problem(T, K, N, dz1 ? 2 : 1, plan.split), ws);
     a.late_wait = plan.beside;
+    a.gate = plan.beside ? ws.gate : nullptr;
     const char* name = dz1 ? "gated_wgrad" : "linear_wgrad";
     const cudaError_t e =
         f32 ? launch<kF32, true, true, 256>(m, a, name, st) : launch<kPlain, true, true, 256>(m, a, name, st);

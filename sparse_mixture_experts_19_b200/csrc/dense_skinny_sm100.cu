@@ -66,6 +66,7 @@ struct Args {
     bf16* z1;
     uint32_t tmem_cols;
     int32_t* flags;
+    uint32_t* gate;  // to open for a weight gradient beside this kernel, or null
 };
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_skinny_kernel(const __grid_
         tmem_relinquish();
     }
     chain_wait();
+    if (a.gate && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == kThreads - 1) gate_open(a.gate);
     chain_next();
     tc_fence_before();
     __syncthreads();
@@ -424,9 +426,11 @@ cudaError_t launch_fwd_skinny(const Geometry& g, const void* x, const void* w0, 
 }
 
 cudaError_t launch_dgrad_skinny(const Geometry& g, const void* dz0, const void* dz1, const void* w0, const void* w1,
-                                int64_t T, int K, int N, void* dx, int32_t* flags, cudaStream_t st) {
+                                int64_t T, int K, int N, void* dx, bool opens_gate, const DenseWs& ws,
+                                cudaStream_t st) {
     Args a{};
-    fill(a, g, T, K, N, dz1 ? 2 : 1, false, flags);
+    fill(a, g, T, K, N, dz1 ? 2 : 1, false, ws.flags);
+    a.gate = opens_gate ? ws.gate : nullptr;
     a.y = static_cast<bf16*>(dx);
     CUtensorMap A0, A1, B0, B1;
     if (!make_tile_map(&A0, false, w0, K, N, 1, 64) || !make_tile_map(&B0, false, dz0, N, T, 1, a.tn))
@@ -524,8 +528,8 @@ cudaError_t launch_dense_dgrad(const void* dz0, const void* dz1, const void* w0,
                                cudaStream_t st) {
     const DgradPlan p = plan_dgrad(T, K, N, dz1 ? 2 : 1, with_wgrad);
     *plan = p.w;
-    return p.c.few ? launch_dgrad_skinny(p.c.g, dz0, dz1, w0, w1, T, K, N, dx, ws.flags, st)
-                   : launch_dense_dgrad_pairs(dz0, dz1, w0, w1, T, K, N, dx, ws, st);
+    return p.c.few ? launch_dgrad_skinny(p.c.g, dz0, dz1, w0, w1, T, K, N, dx, p.w.beside, ws, st)
+                   : launch_dense_dgrad_pairs(dz0, dz1, w0, w1, T, K, N, dx, p.w.beside, ws, st);
 }
 
 }  // namespace moe

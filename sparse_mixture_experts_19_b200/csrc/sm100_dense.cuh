@@ -32,9 +32,37 @@ __device__ __forceinline__ bool aborted_warp(volatile int* abort_flag) {
 // visible.  chain_next lets the kernel after it start in the same way, once
 // every CTA of this one has called it.  Every kernel calls chain_wait first and
 // chain_next second: a kernel that has started then knows that the one before
-// the one before it has completed.
+// the one before it has completed.  That one's writes are promised to who called
+// chain_wait, though, so a kernel that uses them without waiting for the one
+// between takes them over from it through a gate: a thread of the one between
+// opens it (release) after its chain_wait, and the other waits for that (acquire).
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A gate: {open, CTAs that have passed}, both zero between calls.
+__device__ __forceinline__ void gate_open(uint32_t* gate) {
+    asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(gate) : "memory");
+}
+// One thread per CTA; false if the gate stays shut for a second or more.
+constexpr uint32_t kGatePolls = 1u << 21;
+__device__ __forceinline__ bool gate_wait(const uint32_t* gate) {
+    for (uint32_t i = 0; i < kGatePolls; ++i) {
+        uint32_t open;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(open) : "l"(gate) : "memory");
+        if (open) return true;
+    }
+    return false;
+}
+// After gate_wait, by the same threads: the last of the grid's CTAs shuts it.
+__device__ __forceinline__ void gate_passed(uint32_t* gate) {
+    if (atomicAdd(gate + 1, 1u) == gridDim.x - 1) {
+        gate[1] = 0;
+        gate[0] = 0;
+    }
+}
+// Orders what this thread has seen of global memory before its later
+// asynchronous copies from there.
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // ------------------------------------------------------------ TMA stores
 // Tiled 3-D store of a shared-memory box to (c0, c1, c2); elements outside the

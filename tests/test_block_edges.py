@@ -174,3 +174,48 @@ def test_neighbours_and_in_place(gpu_lib):
         for i in range(3):
             a = [x.clone(), dy.clone(), dr.clone()]
             assert all(torch.equal(p, q) for p, q in zip(grads(*a, a[i]), want)), (H, i)
+
+
+# ------------------------------------- the weight gradient beside the other
+@pytest.mark.parametrize("T,K,N", [(1, 2048, 768), (65, 2048, 768), (1000, 264, 136), (1500, 2048, 768),
+                                   (3000, 520, 264)])
+def test_operands_written_just_before(gpu_lib, T, K, N):
+    """A weight gradient that starts beside the input gradient reads what the
+    kernels before both have written: x by a norm chained in front, dg and du by
+    the call's own first kernel.  The bits are those of calls with a wait in
+    between, and each call leaves the workspace's header clear."""
+    moe, g = gpu_lib, gen_of(T + K)
+    rounds = 8
+    src = [rnd(g, T, K) for _ in range(rounds)]
+    w, wu, dy, u = rnd(g, N, K, scale=K ** -0.5), rnd(g, N, K, scale=K ** -0.5), rnd(g, T, N), rnd(g, T, N)
+    ncfg, cfg = moe.norm_config(T, K, "rms"), moe.dense_config(T, K, N, "none")
+    gcfg = moe.dense_config(T, K, N, "silu")
+    ws = moe._new_ws(max(moe.moe_linear_backward_workspace_size(cfg), moe.moe_gated_backward_workspace_size(gcfg)),
+                     "cuda")
+    x = torch.empty_like(src[0])
+
+    def step(i, wait):
+        out = [torch.empty_like(x), torch.empty((N, K), device="cuda")]
+        out += [torch.empty_like(x), torch.empty((N, K), device="cuda"), torch.empty((N, K), device="cuda")]
+        for call in (lambda: moe.moe_norm_forward(ncfg, src[i], None, None, x),
+                     lambda: moe.moe_linear_backward(cfg, dy, x, w, None, *out[:2], None, ws),
+                     lambda: moe.moe_gated_backward(gcfg, dy, x, w, wu, dy, u, *out[2:], ws=ws)):
+            call()
+            if wait:
+                torch.cuda.synchronize()
+                assert (ws[:moe.DENSE_WS_HEADER] == 0).all()
+        return out
+
+    want = [step(i, True) for i in range(rounds)]
+    for _ in range(4):
+        got = [step(i, False) for i in range(rounds)]
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [step(i, False) for i in range(rounds)]
+    for _ in range(2):
+        graph.replay()
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    assert (ws[:moe.DENSE_WS_HEADER] == 0).all()
