@@ -136,26 +136,41 @@ inline bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64
 }
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel (by
-// address), device and size.
+// address), device and size.  One entry per kernel, however many devices use it:
+// the norm kernels alone are 56 of one type, and share this table.
 template <typename Kernel>
 inline cudaError_t ensure_smem_attr(Kernel kernel, size_t bytes) {
     struct Done {
         const void* fn;
-        int dev;
-        size_t bytes;
+        size_t bytes;   // the most asked for
+        uint64_t devs;  // devices (below 64) that have it
     };
-    static Done done[64];
+    constexpr int kKernels = 64;
+    static Done done[kKernels];
     static int n = 0;
     static std::mutex mu;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     const void* fn = reinterpret_cast<const void*>(kernel);
     std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < n; ++i)
-        if (done[i].fn == fn && done[i].dev == dev && done[i].bytes >= bytes) return cudaSuccess;
+    int i = 0;
+    while (i < n && done[i].fn != fn) ++i;
+    const bool known = i < n;
+    if (known && done[i].bytes >= bytes) {
+        if (done[i].devs & bit) return cudaSuccess;
+        bytes = done[i].bytes;
+    }
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && n < 64) done[n++] = Done{fn, dev, bytes};
+    if (e != cudaSuccess) return e;
+    if (!known) {
+        if (n == kKernels) return e;
+        done[n++] = Done{fn, bytes, 0};
+    } else if (bytes > done[i].bytes) {
+        done[i] = Done{fn, bytes, 0};
+    }
+    done[i].devs |= bit;
     return e;
 }
 

@@ -2,6 +2,7 @@
 import ctypes
 import os
 import re
+import subprocess
 import types
 
 import pytest
@@ -110,3 +111,51 @@ def test_overlap_without_rows():
     lib, cfg = moe.load(), moe.dense_config(0, K, N)
     a = [None, None, G, None, None, G, None]
     assert lib.moe_linear_backward(ctypes.byref(cfg), *a, 2 * G, 1 << 40, None) == 1
+
+
+# ------------------------------------------------- kernels' shared memory
+SMEM_ATTR = r"""
+#include <cuda_runtime.h>
+#include <stdio.h>
+static int device = 0, sets = 0, last = 0;
+static cudaError_t get_device(int* d) { *d = device; return cudaSuccess; }
+template <typename F> static cudaError_t set_attribute(F, cudaFuncAttribute, int bytes) {
+    ++sets;
+    last = bytes;
+    return cudaSuccess;
+}
+#define cudaGetDevice get_device
+#define cudaFuncSetAttribute set_attribute
+#include "tma_host.cuh"
+template <int I> void kernel(int* p) { *p = I; }
+template <int I> struct Each {
+    static void run(size_t bytes) {
+        moe::ensure_smem_attr(kernel<I>, bytes);
+        Each<I - 1>::run(bytes);
+    }
+};
+template <> struct Each<-1> { static void run(size_t) {} };
+int main() {
+    for (int round = 0; round < 3; ++round)
+        for (device = 0; device < 3; ++device) Each<55>::run(1000);
+    printf("%d ", sets);
+    device = 1;
+    Each<0>::run(2000);  // more: set anew, on each device
+    Each<0>::run(1500);
+    device = 2;
+    Each<0>::run(1500);
+    Each<0>::run(2000);
+    printf("%d %d\n", sets, last);
+}
+"""
+
+
+def test_shared_memory_attribute_on_several_devices(tmp_path):
+    """56 kernels of one type on three devices: the attribute is set once for
+    each, and the largest size asked for is what later devices get."""
+    src = tmp_path / "attr.cpp"
+    src.write_text(SMEM_ATTR)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(build._nvcc())))
+    subprocess.run(["g++", "-std=c++17", "-O0", "-w", f"-I{cuda}/include", f"-I{build.CSRC}", str(src), "-o",
+                    str(tmp_path / "attr"), f"-L{cuda}/lib64", "-lcudart", f"-Wl,-rpath,{cuda}/lib64"], check=True)
+    assert subprocess.check_output([str(tmp_path / "attr")], text=True).split() == ["168", "170", "2000"]
