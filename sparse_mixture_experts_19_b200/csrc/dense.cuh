@@ -50,7 +50,7 @@ struct DenseDzArgs {
     const bf16* dy;          // [T, N]
     const bf16* z;           // [T, N] pre-activations (gated: g)
     const bf16* u;           // gated
-    bf16* dz;                // [T, N] (gated: dg); null: column sums alone
+    bf16* dz;                // [T, N] (gated: dg); not written for a linear layer without activation
     bf16* dz1;               // gated: du
     float* part;             // [dense_dz_row_blocks][1 or 2][N]
 };

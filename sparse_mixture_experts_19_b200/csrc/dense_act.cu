@@ -44,9 +44,9 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// kAct: the activation; kGated: dg and du from dh, g, u; kStore: write dz
-// (false: column sums of dy alone, kAct none).
-template <int kAct, bool kGated, bool kStore>
+// kAct: the activation; kGated: dg and du from dh, g, u.  A linear layer without
+// an activation has dy itself for dz: column sums alone.
+template <int kAct, bool kGated>
 __global__ void __launch_bounds__(32 * kLanes, kGated ? kBlocksGated : kBlocksLinear) dense_dz_kernel(const DenseDzArgs a) {
     __shared__ float red[kLanes][kCols + 4];
     sm100::chain_wait();
@@ -80,13 +80,11 @@ __global__ void __launch_bounds__(32 * kLanes, kGated ? kBlocksGated : kBlocksLi
                     s0[j] += d[j];
                 }
             }
-            if (kStore) {
-                if (kGated) {
-                    *reinterpret_cast<uint4*>(a.dz + o) = pack8(z);
-                    *reinterpret_cast<uint4*>(a.dz1 + o) = pack8(d);
-                } else {
-                    *reinterpret_cast<uint4*>(a.dz + o) = pack8(d);
-                }
+            if (kGated) {
+                *reinterpret_cast<uint4*>(a.dz + o) = pack8(z);
+                *reinterpret_cast<uint4*>(a.dz1 + o) = pack8(d);
+            } else if (kAct != MOE_ACT_NONE) {
+                *reinterpret_cast<uint4*>(a.dz + o) = pack8(d);
             }
         }
     }
@@ -119,14 +117,12 @@ int dense_dz_row_blocks(int64_t T, int64_t N, bool gated) {
 cudaError_t launch_dense_dz(DenseDzArgs a, bool gated, int act, float* db0, float* db1, cudaStream_t st) {
     const int rb = dense_dz_row_blocks(a.T, a.N, gated);
     a.rows_per_block = (a.T + rb - 1) / rb;
-    const bool store = a.dz != nullptr;
     if (!(db0 || db1)) a.part = nullptr;
     const dim3 grid((a.N + kCols - 1) / kCols, rb), block(32, kLanes);
     trace_before(gated ? "gated_dgu" : "linear_dz", st);
     cudaError_t e = cudaSuccess;
     by_act(act, [&](auto k) {
-        auto* fn = gated ? dense_dz_kernel<k.value, true, true>
-                         : (store ? dense_dz_kernel<k.value, false, true> : dense_dz_kernel<MOE_ACT_NONE, false, false>);
+        auto* fn = gated ? dense_dz_kernel<k.value, true> : dense_dz_kernel<k.value, false>;
         e = launch_chained(fn, grid, block, 0, 0, st, a);
     });
     trace_after(st);

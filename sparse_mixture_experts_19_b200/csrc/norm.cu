@@ -80,30 +80,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// 8 consecutive elements of a row as they lie in memory.
-template <typename X>
-struct Raw8 {
-    uint4 q[sizeof(X) / 2];
-    __device__ __forceinline__ void load(const X* p) {
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof(X) / 2); ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        if constexpr (sizeof(X) == 4) {
-            const uint32_t u[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
-        } else {
-            const uint32_t u[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(u[i] << 16);
-                v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-            }
-        }
-    }
-};
-
 // A thread's columns of a float32 vector, or `other` where there is none.
 template <int kVpt>
 __device__ __forceinline__ void load_cols(float (&v)[kVpt][8], const float* p, int t, int threads, int H, float other) {
