@@ -330,11 +330,14 @@ struct Geometry {
 
 // Token tiles of tn, the reduction split over the largest cluster whose
 // clusters all fit on the GPU at once, with at least 4 steps per CTA.  The
-// estimate is a fit to 220 measured calls (both forward forms, T = 100 ... 800,
-// five weight shapes from 1024 x 1024 to 8192 x 2048, tiles of 64 to 256 tokens;
-// rms error 9%): a step is the slowest of issuing it (0.29 us), its MMAs and its
-// bytes at the rate that the SMs draw from L2 together; then the partial sums
-// that come from peers, and the tile's way out of TMEM and through the epilogue.
+// estimate began as a fit to 220 measured calls (both forward forms, T = 100 ...
+// 800, five weight shapes from 1024 x 1024 to 8192 x 2048, tiles of 64 to 256
+// tokens); the rates and issue times below came later, from the calls named there.
+// Of the layouts that it chooses now, on six shapes from 768 x 2048 to 8192 x 2048,
+// its rms error is 9% for 83 forward calls of 100 to 1000 rows, 13% for 48 of fewer
+// and 8% for 77 input gradients.  A step is the slowest of issuing it (0.29 us), its
+// MMAs and its bytes at the rate that the SMs draw from L2 together; then the partial
+// sums that come from peers, and the tile's way out of TMEM and through the epilogue.
 // The weights come from HBM at 6.2 TB/s for one token tile, at 5.0 for several
 // (gate/up, 64 rows: 14336 -> 4096 takes 42.4 us in one tile and 52.3 in two, but
 // 2880 -> 2880, bound by its steps, 13.2 and 12.0).  Issuing a step of a two-step

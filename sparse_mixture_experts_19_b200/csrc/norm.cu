@@ -12,8 +12,9 @@
 // built around bytes in flight: one CTA per SM, whose 16 warps form groups of
 // W warps, one row per group at a time.  Each group has a ring of S row slots
 // in shared memory that one thread fills with bulk copies (rows are
-// contiguous), up to 80 KB (backward: 200 KB) per SM on their way whatever the
-// registers hold.
+// contiguous), so that 64 to 96 KB of an SM's bf16 rows (float32: up to 192;
+// backward: up to 200; less where the rows are shorter than 512 elements) are on
+// their way whatever the registers hold.
 // A row is read from HBM once; its statistics (forward: the mean, then the
 // squared deviations from it, so no cancellation; backward: the two sums) are
 // warp sums joined through shared memory with one barrier of the group each,
@@ -39,8 +40,8 @@ using namespace sm100;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRingBytes = 200 * 1024;
-// The forward's ring (two rows per group at least): 80 KB per SM are what HBM's
-// latency asks for, and reading further ahead of the writes mostly costs (bf16,
+// The forward's ring, as far as whole rows fill it (but two per group at least, three
+// per group of 8 or 16 warps): 80 KB per SM are what HBM's latency asks for, and reading further ahead of the writes mostly costs (bf16,
 // RMS form: 16384 rows of 2880 take 32.5 us with 80 KB and 35.2 with 200, 16384 of
 // 4096 42.7 and 47.4; but 65536 of 1024 47.3 and 45.0).
 constexpr int kFwdRingBytes = 80 * 1024;
