@@ -8,10 +8,11 @@ import math
 import pytest
 import torch
 
-from test_block_ops import (ACTS, BF, F32, U8, U24, acc_tol, act64, canary_intact, gen_of, guarded, norm64, rnd,
+from test_block_ops import (ACTS, BF, F32, U8, acc_tol, gen_of, rnd,
                             test_gated_backward as check_gated_backward, test_gated_forward as check_gated_forward,
                             test_linear_backward as check_linear_backward,
-                            test_linear_forward as check_linear_forward, within)
+                            test_linear_forward as check_linear_forward, test_norm_backward as check_norm_backward,
+                            test_norm_forward as check_norm_forward, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -219,3 +220,151 @@ def test_operands_written_just_before(gpu_lib, T, K, N):
     for a, b in zip(got, want):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
     assert (ws[:moe.DENSE_WS_HEADER] == 0).all()
+
+
+# -------------------------------------------- rings used again and again
+# more rows per group of warps than its ring has slots, and then some: the slots
+# are filled again and their barriers change phase, at every number of warps per row
+@pytest.mark.parametrize("T,H,kind,dt", [(24000, 512, "layer", BF), (20000, 264, "rms", F32), (12000, 1024, "rms", BF),
+                                         (8000, 2056, "layer", BF), (4000, 2880, "rms", BF), (2500, 4104, "layer", F32),
+                                         (1300, 8200, "layer", BF), (1300, 16384, "rms", BF), (800, 16384, "layer", F32)])
+def test_norm_of_many_rows(gpu_lib, T, H, kind, dt):
+    check_norm_forward(gpu_lib, T, H, kind, dt, "wb")
+    check_norm_backward(gpu_lib, T, H, kind, dt, False, False)
+    check_norm_backward(gpu_lib, T, H, kind, dt, True, True)
+
+
+# ------------------------------------------------- the form a product takes
+def kernels(moe, call):
+    """Names of the kernels that a call launches."""
+    moe.moe_trace_begin(64)
+    call()
+    return [name for name, _ in moe.moe_trace_end()]
+
+
+def form_of(moe, op, T, K, N):
+    x, w = torch.zeros((T, K), dtype=BF, device="cuda"), torch.zeros((N, K), dtype=BF, device="cuda")
+    return kernels(moe, (lambda: moe.linear(x, w)) if op == "linear" else (lambda: moe.gated(x, w, w)))
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T,K,N,split", [(2000, 1000, 1016, False), (4000, 520, 1288, False), (700, 2880, 5000, False),
+                                         (1030, 3200, 4104, True)])
+def test_linear_of_many_rows(gpu_lib, T, K, N, split, act):
+    """Tiles of 128 and of 256 columns, ragged on both sides; tiles split along
+    the reduction."""
+    assert form_of(gpu_lib, "linear", T, K, N) == ["linear_fwd"]
+    cfg = gpu_lib.dense_config(T, K, N)
+    assert (gpu_lib.moe_linear_workspace_size(cfg) > gpu_lib.DENSE_WS_HEADER) == split
+    check_linear_forward(gpu_lib, T, K, N, act)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T,K,N,form,split", [
+    (2000, 328, 1000, "gated_fwd", False), (2600, 136, 1032, "gated_fwd", False), (1500, 4104, 2056, "gated_fwd", True),
+    (129, 264, 1032, "gated_fwd_skinny", False), (17, 2048, 520, "gated_fwd_skinny", False)])
+def test_gated_forms(gpu_lib, T, K, N, form, split, act):
+    """Every activation in both forms of the gate/up kernel."""
+    assert form_of(gpu_lib, "gated", T, K, N) == [form]
+    cfg = gpu_lib.dense_config(T, K, N, act)
+    assert (gpu_lib.moe_gated_workspace_size(cfg) > gpu_lib.DENSE_WS_HEADER) == split
+    check_gated_forward(gpu_lib, T, K, N, act)
+
+
+@pytest.mark.parametrize("T,K,N,names", [
+    (65, 2048, 768, ["gated_dgu", "gated_dgrad_skinny", "gated_wgrad"]),
+    (1000, 264, 136, ["gated_dgu", "gated_dgrad_skinny", "gated_wgrad", "wgrad_sum"]),
+    (2000, 2048, 768, ["gated_dgu", "gated_dgrad", "gated_wgrad"]),
+    (2000, 520, 264, ["gated_dgu", "gated_dgrad", "gated_wgrad", "wgrad_sum"])])
+def test_gated_backward_forms(gpu_lib, T, K, N, names):
+    moe, g = gpu_lib, gen_of(25)
+    cfg = moe.dense_config(T, K, N, "gelu")
+    t, w = rnd(g, T, N), rnd(g, N, K)
+    dw = [torch.empty((N, K), device="cuda") for _ in range(2)]
+    ws = moe.gated_backward_workspace(cfg)
+    x = rnd(g, T, K)
+    assert kernels(moe, lambda: moe.moe_gated_backward(cfg, t, x, w, w, t, t, torch.empty_like(x), *dw, ws=ws)) == names
+    check_gated_backward(moe, T, K, N, "gelu", "f32")
+
+
+@pytest.mark.parametrize("T,K,N,names", [
+    (1000, 264, 136, ["linear_dz", "linear_dgrad_skinny", "linear_wgrad", "wgrad_sum"]),
+    (1500, 2048, 768, ["linear_dz", "linear_dgrad", "linear_wgrad"]),
+    (3000, 520, 264, ["linear_dz", "linear_dgrad", "linear_wgrad", "wgrad_sum"])])
+def test_linear_backward_forms(gpu_lib, T, K, N, names):
+    moe, g = gpu_lib, gen_of(27)
+    cfg = moe.dense_config(T, K, N, "silu")
+    x, t, w, dw = rnd(g, T, K), rnd(g, T, N), rnd(g, N, K), torch.empty((N, K), device="cuda")
+    ws = moe.linear_backward_workspace(cfg)
+    assert kernels(moe, lambda: moe.moe_linear_backward(cfg, t, x, w, t, torch.empty_like(x), dw, None, ws)) == names
+    check_linear_backward(moe, T, K, N, "silu", "f32")
+
+
+def test_one_workspace_for_split_products(gpu_lib):
+    """Calls whose tiles are split 2, 3 and 8 ways, on different numbers of
+    tiles, one after another in one workspace: the counters of each are back at
+    zero when it ends, and its bits are those of a workspace of its own."""
+    moe, g = gpu_lib, gen_of(26)
+    calls = []
+
+    def operands(T, K, N):
+        return (rnd(g, T, K), *(rnd(g, N, K, scale=K ** -0.5) for _ in range(2)), *(rnd(g, T, N) for _ in range(3)))
+
+    for T, K, N in ((1500, 2880, 3304), (300, 18432, 4944), (1030, 3200, 4104)):
+        x, w, _, _, _, res = operands(T, K, N)
+        cfg = moe.dense_config(T, K, N)
+        assert form_of(moe, "linear", T, K, N) == ["linear_fwd"]
+        calls.append((moe.moe_linear_workspace_size(cfg),
+                      lambda ws, x=x, w=w, res=res: [moe.linear(x, w, None, res, "silu", ws=ws)]))
+    for T, K, N in ((1500, 4104, 2056), (1030, 3200, 2056)):
+        x, w, wu, _, _, _ = operands(T, K, N)
+        assert form_of(moe, "gated", T, K, N) == ["gated_fwd"]
+        calls.append((moe.moe_gated_workspace_size(moe.dense_config(T, K, N, "silu")),
+                      lambda ws, x=x, w=w, wu=wu: [moe.gated(x, w, wu, ws=ws)]))
+    for T, K, N in ((1030, 4104, 2056), (2000, 2880, 2880)):
+        x, w, wu, dh, gg, u = operands(T, K, N)
+        cfg = moe.dense_config(T, K, N, "silu", grad_dtype="bf16")
+
+        def backward(ws, cfg=cfg, x=x, w=w, wu=wu, dh=dh, gg=gg, u=u):
+            out = [torch.empty_like(t) for t in (x, w, wu)]
+            moe.moe_gated_backward(cfg, dh, x, w, wu, gg, u, *out, ws=ws)
+            return out
+
+        calls.append((moe.moe_gated_backward_workspace_size(cfg), backward))
+        names = kernels(moe, lambda: backward(moe.gated_backward_workspace(cfg)))
+        assert "gated_dgrad" in names and "gated_dgrad_skinny" not in names
+    assert all(n > moe.DENSE_WS_HEADER for n, _ in calls)
+    want = [call(moe._new_ws(n, "cuda")) for n, call in calls]
+    ws = moe._new_ws(max(n for n, _ in calls), "cuda")
+    for order in (range(len(calls)), reversed(range(len(calls)))):
+        for i in order:
+            got = calls[i][1](ws)
+            assert (ws[:moe.DENSE_WS_HEADER] == 0).all(), i
+            assert all(torch.equal(p, q) for p, q in zip(got, want[i])), i
+
+
+# ---------------------------------------------------- long reductions, normwise
+@pytest.mark.parametrize("T,K,N", [(300, 18432, 4944), (33, 16392, 264), (2100, 264, 16392), (40, 136, 16392),
+                                   (20000, 264, 136), (16391, 72, 520)])
+def test_long_reductions_normwise(gpu_lib, T, K, N):
+    """The whole tensor's error over its norm, where one element's bound is wide.
+    Step j of a reduction of n = K / 16 steps is off by at most 17 units of 2^-23 of
+    the sum so far, of norm sqrt(j / n) of the result's for independent terms
+    (on average 2/3), and of its own 16 terms' sizes (under 0.43 of it from 64 steps
+    on): 17 * 2^-23 * n * 1.1 in all, and the rounding's 2^-8.  One 64-deep step left
+    out of 18432 would be 0.059."""
+    moe, g = gpu_lib, gen_of(T + K + N)
+    x, w, dy = rnd(g, T, K), rnd(g, N, K, scale=K ** -0.5), rnd(g, T, N)
+
+    def close(got, ref, depth, what):
+        err = (got.double() - ref).norm() / ref.norm()
+        assert err <= U8 + 17 * 2.0 ** -23 * max(depth / 16, 1) * 1.1, (what, float(err))
+
+    u = torch.empty_like(dy)
+    close(moe.linear(x, w), x.double() @ w.double().t(), K, "y")
+    moe.gated(x, w, w, act="none", u_out=u)
+    close(u, x.double() @ w.double().t(), K, "u")
+    cfg, dx, dw = moe.dense_config(T, K, N), torch.empty_like(x), torch.empty((N, K), device="cuda")
+    moe.moe_linear_backward(cfg, dy, x, w, None, dx, dw, None, moe.linear_backward_workspace(cfg))
+    close(dx, dy.double() @ w.double(), N, "dx")
+    close(dw, dy.double().t() @ x.double(), T, "d_w")
