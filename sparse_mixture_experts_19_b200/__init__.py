@@ -191,7 +191,7 @@ def _on(stream):
 
     if stream is None:
         return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
+    if not isinstance(stream, torch.Stream):
         handle = stream if isinstance(stream, int) else stream.cuda_stream
         # 0 and 1 are the default stream's handles (none, cudaStreamLegacy); as an
         # external stream's, 0 would mean "none given": a stream of torch's own

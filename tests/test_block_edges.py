@@ -69,6 +69,9 @@ def test_stream_handles_of_torch_streams(gpu_lib):
     for s in (st, st.cuda_stream, Handle(st.cuda_stream)):
         with moe._on(s):
             assert torch.cuda.current_stream().cuda_stream == st.cuda_stream
+    plain = torch.Stream(device="cuda")  # torch's stream of any device
+    with moe._on(plain):
+        assert torch.cuda.current_stream().stream_id == plain.stream_id
     with torch.cuda.stream(st), moe._on(0):
         assert torch.cuda.current_stream() == torch.cuda.default_stream()
     with moe._on(2):
